@@ -1,7 +1,7 @@
 """Python binding of libmmac: tiled dense and 4:2-sparse GEMM for MI355X (gfx950).
 
-Thin ctypes layer over the C ABI in include/mmac.h, with the same entry
-points.  It only marshals arguments: torch tensors provide device memory and
+Thin ctypes layer over the C ABI in include/mmac.h and include/mmac_lowbit.h, with
+the same entry points.  It only marshals arguments: torch tensors provide device memory and
 the current HIP stream; every step of the computation runs in the library's
 HIP kernels.  If libmmac.so is missing, importing the binding succeeds but the
 first call raises -- there is no fallback path.
@@ -14,6 +14,9 @@ Tensor conventions (element strides; the last dimension must be contiguous):
                variants: D's dtype picks the output type, C has D's dtype),
                plus an optional fp32 bias of N values and ReLU
     Ac  M x K/2, idx M x ceil(K/32) int32/uint32 words
+    4-bit weights   codes N x 16 ceil(K/32) uint8, scale words groups x N int32
+    8-bit activations   elements M x 32 ceil(K/32) (float8_e4m3fn, float8_e5m2 or int8),
+               scale words ceil(K/128) x M int32
 """
 import ctypes
 import os
@@ -24,6 +27,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libmmac.so")
 
 F16, BF16, I8, FP8_E4M3, BF8_E5M2, FP4_E2M1, FP6_E2M3, BF6_E3M2 = 1, 2, 3, 4, 5, 6, 7, 8
+U4, F32 = 9, 10
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_MISALIGNED, ERR_HIP, ERR_SCRATCH = 0, 1, 2, 3, 4, 5
 
 OUT_ACC, OUT_BF16, OUT_F16, OUT_FP8_E4M3, OUT_BF8_E5M2 = 0, 1, 2, 3, 4
@@ -41,6 +45,12 @@ _lib = None
 class Epilogue(ctypes.Structure):
     """mmac_epilogue_t."""
     _fields_ = [("d_type", ctypes.c_int32), ("act", ctypes.c_int32), ("bias", ctypes.c_void_p)]
+
+
+class W4(ctypes.Structure):
+    """mmac_w4_t."""
+    _fields_ = [("q_type", ctypes.c_int32), ("group", ctypes.c_int32), ("codes", ctypes.c_void_p),
+                ("pitch", ctypes.c_int64), ("words", ctypes.c_void_p), ("ldw", ctypes.c_int64)]
 
 
 class MmacError(RuntimeError):
@@ -89,6 +99,22 @@ def lib():
                                              vp, i64, ep, vp]
         L.mmac_gemm_workspace_bytes.restype = i64
         L.mmac_gemm_workspace_bytes.argtypes = [i32, i64, i64, i64, i32]
+        w4 = ctypes.POINTER(W4)
+        L.mmac_w4_quantize.restype = i32
+        L.mmac_w4_quantize.argtypes = [i32, i32, i64, i64, vp, i64, w4, vp]
+        L.mmac_gemm_w4.restype = i32
+        L.mmac_gemm_w4.argtypes = [i32, i64, i64, i64, dbl, vp, i64, w4, dbl, vp, i64, vp, i64, ep, vp, i64, vp]
+        L.mmac_gemm_w4_workspace_bytes.restype = i64
+        L.mmac_gemm_w4_workspace_bytes.argtypes = [i64, i64, i64]
+        L.mmac_mx8_quantize.restype = i32
+        L.mmac_mx8_quantize.argtypes = [i32, i32, i64, i64, vp, i64, vp, i64, vp, i64, vp]
+        L.mmac_mx8_dequantize.restype = i32
+        L.mmac_mx8_dequantize.argtypes = [i32, i32, i64, i64, vp, i64, vp, i64, vp, i64, vp]
+        L.mmac_gemm_mx8_wgrad.restype = i32
+        L.mmac_gemm_mx8_wgrad.argtypes = [i32, i32, i64, i64, i64, dbl, vp, i64, vp, i64, vp, i64, dbl, vp, i64, vp,
+                                          i64, ep, vp, i64, vp]
+        L.mmac_gemm_mx8_wgrad_workspace_bytes.restype = i64
+        L.mmac_gemm_mx8_wgrad_workspace_bytes.argtypes = [i64, i64, i64]
         L.mmac_status_string.restype = ctypes.c_char_p
         L.mmac_status_string.argtypes = [i32]
         _lib = L
@@ -362,6 +388,152 @@ def gemm_layout(A, B, D, trans_a=False, trans_b=False, alpha=1.0, beta=0.0, C=No
                                       _ld(A), _ptr(B), _ld(B), float(beta), _ptr(C), _ld(C) if C is not None else 0,
                                       _ptr(D), _ld(D), None if ep is None else ctypes.byref(ep), _stream(stream))
     _check(st, "mmac_gemm_dense_layout")
+    return D
+
+
+# ---- low-bit operands (include/mmac_lowbit.h) ----------------------------------------------------
+
+def _current_device(*tensors):
+    """Every tensor lives on the current CUDA device, the one the call's stream belongs to."""
+    _same_device(*tensors)
+    for t in tensors:
+        if t is not None and t.device.index != torch.cuda.current_device():
+            raise ValueError(f"tensors on {t.device}, but the current device is cuda:{torch.cuda.current_device()}")
+
+
+def _input_type(t, given):
+    """Type code of an unquantized matrix."""
+    if given is not None:
+        if t.element_size() != {F32: 4, F16: 2, BF16: 2}.get(given, t.element_size()):
+            raise ValueError(f"a tensor of {t.element_size()}-byte elements for type code {given}")
+        return given
+    if t.dtype not in (torch.float16, torch.bfloat16, torch.float32):
+        raise ValueError(f"expected a float16, bfloat16 or float32 tensor, got {t.dtype}")
+    return F32 if t.dtype == torch.float32 else DTYPE_OF[t.dtype]
+
+
+def _w4(Wq, SW, N, K, group, q_type):
+    """The mmac_w4_t of a weight matrix."""
+    _shape(Wq, N, (K + 31) // 32 * 16, "Wq", min_cols=True)
+    if Wq.element_size() != 1:
+        raise ValueError("Wq must hold bytes, two codes each")
+    if SW.element_size() != 4:
+        raise ValueError("SW must hold 32-bit scale words")
+    _shape(SW, 1 if group == 0 else (K + group - 1) // group, N, "SW", min_cols=True)
+    return W4(q_type, group, Wq.data_ptr(), max(_ld(Wq), 16), SW.data_ptr(), _ld(SW))
+
+
+def _workspace_tensor(nbytes, device):
+    if nbytes == 0:
+        return None
+    return torch.zeros(nbytes, dtype=torch.uint8, device=device if device is not None else torch.device("cuda"))
+
+
+def _workspace_args(workspace):
+    return (None, 0) if workspace is None else (_ptr(workspace), workspace.numel() * workspace.element_size())
+
+
+def w4_quantize(W, Wq, SW, group=128, q_type=U4, symmetric=False, w_type=None, stream=None):
+    """Weights W (N x K, float16, bfloat16 or float32) to 4-bit codes Wq (N x 16 ceil(K/32) uint8) and
+    scale words SW (groups x N int32), one per `group` (32, 64, 128; 0: whole rows) elements of a
+    row, rounded to nearest.  q_type U4 (symmetric: zero point 8) or FP4_E2M1 (symmetric)."""
+    N, K = W.shape
+    q = _w4(Wq, SW, N, K, group, q_type)
+    _current_device(W, Wq, SW)
+    _check(lib().mmac_w4_quantize(_input_type(W, w_type), int(bool(symmetric or q_type == FP4_E2M1)), N, K, _ptr(W),
+                                  _ld(W), ctypes.byref(q), _stream(stream)), "mmac_w4_quantize")
+    return Wq, SW
+
+
+def w4_workspace_bytes(M, N, K):
+    """Bytes of workspace gemm_w4 uses for this product (0: it would not split)."""
+    return int(lib().mmac_gemm_w4_workspace_bytes(M, N, K))
+
+
+def w4_workspace(M, N, K, device=None):
+    """A zeroed workspace tensor for gemm_w4 (None if it would not split)."""
+    return _workspace_tensor(w4_workspace_bytes(M, N, K), device)
+
+
+def gemm_w4(A, Wq, SW, D, group=128, q_type=U4, alpha=1.0, beta=0.0, C=None, a_type=None, stream=None, bias=None,
+            act=ACT_NONE, d_type=None, workspace=None):
+    """D = round(act(alpha * A @ W.T + beta * C + bias)) with A M x K (float16 or bfloat16) and the weight W (N x K)
+    as w4_quantize stores it.  Epilogue arguments as in gemm_dense; with a workspace (see w4_workspace())
+    K may be split."""
+    M, K = A.shape
+    N = Wq.shape[0]
+    _shape(D, M, N, "D")
+    _shape(C, M, N, "C")
+    _bias(bias, N)
+    _current_device(A, Wq, SW, C, D, bias, workspace)
+    q = _w4(Wq, SW, N, K, group, q_type)
+    ep = _epilogue(D, bias, act, d_type, C)
+    _check(lib().mmac_gemm_w4(_input_type(A, a_type), M, N, K, float(alpha), _ptr(A), _ld(A), ctypes.byref(q),
+                              float(beta), _ptr(C), _ld(C) if C is not None else 0, _ptr(D), _ld(D),
+                              None if ep is None else ctypes.byref(ep), *_workspace_args(workspace), _stream(stream)),
+           "mmac_gemm_w4")
+    return D
+
+
+def _mx8(Xq, SX, M, K, q_type):
+    """Checks an mx8 matrix; returns its element type's code."""
+    _shape(Xq, M, (K + 31) // 32 * 32, "Xq", min_cols=True)
+    if Xq.element_size() != 1 or (q_type is None and Xq.dtype not in DTYPE_OF):
+        raise ValueError(f"Xq must hold float8_e4m3fn, float8_e5m2 or int8 elements, got {Xq.dtype}")
+    if SX.element_size() != 4:
+        raise ValueError("SX must hold 32-bit scale words")
+    _shape(SX, (K + 127) // 128, M, "SX", min_cols=True)
+    return _dtype(Xq, q_type)
+
+
+def mx8_quantize(X, Xq, SX, x_type=None, q_type=None, stream=None):
+    """Activations X (M x K, float16, bfloat16 or float32) to 8-bit elements Xq (M x 32 ceil(K/32),
+    float8_e4m3fn, float8_e5m2 or int8) and scale words SX (ceil(K/128) x M int32): the operand
+    form of gemm_mx, and of gemm_mx8_wgrad."""
+    M, K = X.shape
+    tq = _mx8(Xq, SX, M, K, q_type)
+    _current_device(X, Xq, SX)
+    _check(lib().mmac_mx8_quantize(_input_type(X, x_type), tq, M, K, _ptr(X), _ld(X), _ptr(Xq), _ld(Xq),
+                                   _ptr(SX), _ld(SX), _stream(stream)), "mmac_mx8_quantize")
+    return Xq, SX
+
+
+def mx8_dequantize(Xq, SX, X, q_type=None, x_type=None, stream=None):
+    """The activations that (Xq, SX) stand for, rounded to X's type; X gives M and K."""
+    M, K = X.shape
+    tq = _mx8(Xq, SX, M, K, q_type)
+    _current_device(X, Xq, SX)
+    _check(lib().mmac_mx8_dequantize(tq, _input_type(X, x_type), M, K, _ptr(Xq), _ld(Xq), _ptr(SX),
+                                     _ld(SX), _ptr(X), _ld(X), _stream(stream)), "mmac_mx8_dequantize")
+    return X
+
+
+def mx8_wgrad_workspace_bytes(M, N, K):
+    """Bytes of workspace gemm_mx8_wgrad uses for this product (0: it would not split)."""
+    return int(lib().mmac_gemm_mx8_wgrad_workspace_bytes(M, N, K))
+
+
+def mx8_wgrad_workspace(M, N, K, device=None):
+    """A zeroed workspace tensor for gemm_mx8_wgrad (None if it would not split)."""
+    return _workspace_tensor(mx8_wgrad_workspace_bytes(M, N, K), device)
+
+
+def gemm_mx8_wgrad(dY, Xq, SX, D, alpha=1.0, beta=0.0, C=None, y_type=None, q_type=None, stream=None, d_type=None,
+                   workspace=None):
+    """Weight gradient D = alpha * dY.T @ X + beta * C (N x K) from the gradient dY (M x N, float16 or bfloat16) of a
+    linear layer's output and its input as mx8_quantize stored it; D gives K."""
+    M, N = dY.shape
+    K = D.shape[1]
+    tq = _mx8(Xq, SX, M, K, q_type)
+    _shape(D, N, K, "D")
+    _shape(C, N, K, "C")
+    _current_device(dY, Xq, SX, C, D, workspace)
+    ep = _epilogue(D, None, ACT_NONE, d_type, C)
+    _check(lib().mmac_gemm_mx8_wgrad(_input_type(dY, y_type), tq, M, N, K, float(alpha), _ptr(dY),
+                                     _ld(dY), _ptr(Xq), _ld(Xq), _ptr(SX), _ld(SX), float(beta), _ptr(C),
+                                     _ld(C) if C is not None else 0, _ptr(D), _ld(D),
+                                     None if ep is None else ctypes.byref(ep), *_workspace_args(workspace),
+                                     _stream(stream)), "mmac_gemm_mx8_wgrad")
     return D
 
 

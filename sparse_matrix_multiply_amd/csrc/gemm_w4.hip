@@ -1,0 +1,248 @@
+// Products with 4-bit weights and group scales, few rows: D = A * W with W
+// streamed once as codes.
+//
+// With codes n, zero point z and scale s per group g of a weight row j,
+//   sum_k a_ik (n_jk - z_jg) s_jg = sum_g s_jg ( sum_{k in g} a_ik n_jk - z_jg sum_{k in g} a_ik ).
+// Codes 0 .. 15 (and E2M1 values) are exact in bf16 and fp16, so the inner sums run on
+// the 16 x 16 matrix instructions with no rounding of the weight: one
+// accumulator starts at zero in every group, a second one sums A itself (an
+// operand of ones), and at the group's end s * (t - z * u) joins the fp32 total.
+//
+// Codes to 16-bit operands: the byte 0x0n read as E4M3 is n * 2^-9 for every n
+// from 0 to 15 (subnormals up to 7, then the first normal binade), so the
+// instructions that convert pairs of fp8 values with a power-of-two scale give n
+// exactly; E2M1 codes have a conversion of their own.
+//
+// A workgroup owns 16 columns of D and all rows (up to 32); its WK waves split K
+// into contiguous ranges of chunks of 256 elements: of a weight row one 128-byte
+// line, of A 512 bytes.  Each wave copies its chunks straight into a private ring
+// of LDS slots, NSLOT chunks ahead, in whole lines, and reads the fragments back
+// from there; no barrier until the partial tiles are added up in wave order.  The
+// time is that of streaming the codes from HBM.
+#include "gemm_tiled.h"
+#include "lowbit.h"
+
+namespace mmac {
+
+// Eight codes of a word, ascending, as a 16-byte operand of DT values.
+template <int DT, int QT>
+__device__ __forceinline__ i32x4 operand_of(uint32_t w) {
+    i32x4 f;
+    if constexpr (QT == DT_FP4) {
+        if constexpr (DT == DT_BF16) {
+            f[0] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.0f, 0));
+            f[1] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.0f, 1));
+            f[2] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.0f, 2));
+            f[3] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.0f, 3));
+        } else {
+            f[0] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 0));
+            f[1] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 1));
+            f[2] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 2));
+            f[3] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 3));
+        }
+    } else {
+        const uint32_t even = w & 0x0f0f0f0fu, odd = (w >> 4) & 0x0f0f0f0fu;
+        // bytes in ascending order: n0 n1 n2 n3 and n4 n5 n6 n7
+        const uint32_t p0 = __builtin_amdgcn_perm(odd, even, 0x05010400u), p1 = __builtin_amdgcn_perm(odd, even, 0x07030602u);
+        if constexpr (DT == DT_BF16) {
+            f[0] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(p0, 512.0f, false));
+            f[1] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(p0, 512.0f, true));
+            f[2] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(p1, 512.0f, false));
+            f[3] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(p1, 512.0f, true));
+        } else {
+            f[0] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(p0, 512.0f, false));
+            f[1] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(p0, 512.0f, true));
+            f[2] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(p1, 512.0f, false));
+            f[3] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(p1, 512.0f, true));
+        }
+    }
+    return f;
+}
+
+template <int DT>
+__device__ __forceinline__ f32x4 mma16(const i32x4 &a, const i32x4 &b, f32x4 c) {
+    if constexpr (DT == DT_BF16)
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+    else
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+}
+
+// MR rows of A are staged (2, 8, 16 or 32, at least the rows there are); lanes of
+// further rows read staged ones again, and their results are not stored.
+// GROUP 128 also serves whole rows (every chunk then reads word 0).
+template <int DT, int QT, int GROUP, int MR, int WK, int NSLOT>
+__global__ __launch_bounds__(WK * 64) void gemm_w4_rows_kernel(W4Params p) {
+    constexpr int MB = MR > 16 ? 2 : 1;
+    constexpr int GPC = 256 / GROUP;              // groups of a chunk
+    constexpr int SPG = GROUP / 32;               // instruction steps of a group
+    constexpr int SI = (GPC * 16 + 63) / 64;      // copy instructions for scale words
+    constexpr int W_BYTES = 16 * 128, A_BYTES = MR * 512, SLOT = W_BYTES + A_BYTES + SI * 256;
+    constexpr int IPC = 2 + MR / 2 + SI;          // copy instructions of a chunk
+    constexpr int OUTS = MB * 256;
+    constexpr int RED = WK * OUTS * 4;
+    constexpr int LDS_BYTES = WK * NSLOT * SLOT > RED ? WK * NSLOT * SLOT : RED;
+    static_assert(LDS_BYTES <= 160 * 1024 && (NSLOT - 1) * IPC < 64, "LDS and counter range");
+    __shared__ __attribute__((aligned(16))) uint8_t smem[LDS_BYTES];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r16 = lane & 15, q = lane >> 4;
+    const int col0 = blockIdx.x * 16, row0 = blockIdx.y * 32;
+    const int rows = min(p.M - row0, MR), cols = min(16, p.N - col0);
+    const int row_bytes = (p.K + 31) / 32 * 16;
+    const rsrc_t ra = make_rsrc(p.A + row0 * p.a_pitch, (uint32_t)(rows * p.a_pitch));
+    const rsrc_t rw = make_rsrc(p.codes + col0 * p.pitch, (uint32_t)((cols - 1) * p.pitch + row_bytes));
+    const rsrc_t rs = make_rsrc(p.words + col0, (uint32_t)(((p.groups - 1) * p.ldw + cols) * 4));
+
+    f32x4 acc[MB];
+#pragma unroll
+    for (int m = 0; m < MB; ++m) acc[m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+
+    const int nfull = p.K / 256, nall = (p.K + 255) / 256;
+    const int per = (nall + WK - 1) / WK;
+    const int c0 = min(wave * per, nall), c1 = min(c0 + per, nall), c1f = min(c1, nfull);
+    uint8_t *ring = smem + wave * NSLOT * SLOT;
+
+    const auto issue_w = [&](int c, uint8_t *slot) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {   // 8 rows x one line; unit u of row r at u ^ ((r / 2) mod 8)
+            const int r = 8 * j + (lane >> 3);
+            const uint32_t unit = (uint32_t)((lane & 7) ^ ((r >> 1) & 7));
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (lds_void *)(slot + j * 1024), 16,
+                                                     (uint32_t)r * (uint32_t)p.pitch + (uint32_t)c * 128u + unit * 16u, 0, 0, 0);
+        }
+#pragma unroll
+        for (int j = 0; j < SI; ++j) {   // 4 groups x 16 columns of words
+            const int d = j * 64 + lane, g = p.group == 0 ? 0 : c * GPC + (d >> 4);
+            const uint32_t off = d < GPC * 16 && g < p.groups ? (uint32_t)((g * p.ldw + (d & 15)) * 4) : kOutOfRange;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void *)(slot + W_BYTES + A_BYTES + j * 256), 4, off, 0, 0, 0);
+        }
+    };
+    // unit u (8 elements) of row r of A sits at unit u ^ (r mod 16): 16 rows' reads of one unit meet 16 bank groups
+    const auto issue_a = [&](int c, uint8_t *slot) {
+#pragma unroll
+        for (int j = 0; j < MR / 2; ++j) {
+            const int r = 2 * j + (lane >> 5);
+            const uint32_t unit = (uint32_t)((lane & 31) ^ (r & 15));
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void *)(slot + W_BYTES + j * 1024), 16,
+                                                     (uint32_t)r * (uint32_t)p.a_pitch + (uint32_t)c * 512u + unit * 16u, 0, 0, 0);
+        }
+    };
+    constexpr int kOne = DT == DT_BF16 ? 0x3f803f80 : 0x3c003c00;
+    const i32x4 ones = {kOne, kOne, kOne, kOne};
+
+    uint32_t wd[8], sw[GPC];
+    i32x4 a[8][MB];
+    const auto load = [&](const uint8_t *slot) {
+#pragma unroll
+        for (int v = 0; v < 8; ++v) {   // step v: elements 32 v + 8 q .. + 7 of the chunk
+            wd[v] = *reinterpret_cast<const uint32_t *>(slot + r16 * 128 + ((v ^ ((r16 >> 1) & 7)) << 4) + q * 4);
+#pragma unroll
+            for (int m = 0; m < MB; ++m) {
+                const int r = (m * 16 + r16) % MR;
+                a[v][m] = *reinterpret_cast<const i32x4 *>(slot + W_BYTES + r * 512 + (((4 * v + q) ^ (r & 15)) << 4));
+            }
+        }
+#pragma unroll
+        for (int g = 0; g < GPC; ++g)
+            sw[g] = *reinterpret_cast<const uint32_t *>(slot + W_BYTES + A_BYTES + (g * 16 + r16) * 4);
+    };
+    const auto compute = [&]() {
+        const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int g = 0; g < GPC; ++g) {
+            f32x4 t[MB], u[MB];
+#pragma unroll
+            for (int v = g * SPG; v < (g + 1) * SPG; ++v) {
+                const i32x4 b = operand_of<DT, QT>(wd[v]);
+#pragma unroll
+                for (int m = 0; m < MB; ++m) {
+                    t[m] = mma16<DT>(a[v][m], b, v == g * SPG ? zero : t[m]);
+                    if constexpr (QT == DT_U4) u[m] = mma16<DT>(a[v][m], ones, v == g * SPG ? zero : u[m]);
+                }
+            }
+            const float s = __builtin_bit_cast(float, sw[g] & ~0xffu), z = (float)(sw[g] & 0xffu);
+#pragma unroll
+            for (int m = 0; m < MB; ++m)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float x = t[m][i];
+                    if constexpr (QT == DT_U4) x = fmaf(-z, u[m][i], x);
+                    acc[m][i] = fmaf(s, x, acc[m][i]);
+                }
+        }
+    };
+
+#pragma unroll
+    for (int i = 0; i < NSLOT; ++i)
+        if (c0 + i < c1f) {
+            issue_w(c0 + i, ring + i * SLOT);
+            issue_a(c0 + i, ring + i * SLOT);
+        }
+    int slot = 0;
+    for (int c = c0; c < c1f; ++c) {
+        uint8_t *at = ring + slot * SLOT;
+        wait_copies<IPC, NSLOT - 1>(min(NSLOT - 1, c1f - 1 - c));   // chunk c has landed
+        load(at);
+        wait_lds();                                                // read before it is copied over
+        if (c + NSLOT < c1f) {
+            issue_w(c + NSLOT, at);
+            issue_a(c + NSLOT, at);
+        }
+        compute();
+        slot = slot + 1 == NSLOT ? 0 : slot + 1;
+    }
+    if (c0 < c1 && c1 > nfull) {   // the chunk K ends inside: A through registers, zero past K (codes there are finite)
+        issue_w(c1f, ring);
+        for (int j = 0; j < MR / 2; ++j) {
+            const int r = 2 * j + (lane >> 5), unit = lane & 31, e0 = c1f * 256 + unit * 8;
+            *reinterpret_cast<i32x4 *>(ring + W_BYTES + r * 512 + ((unit ^ (r & 15)) << 4)) =
+                masked_unit<2>(ra, (uint32_t)r * (uint32_t)p.a_pitch + (uint32_t)e0 * 2u, e0, p.K);
+        }
+        wait_vm_lgkm0<0>();
+        load(ring);
+        compute();
+    }
+
+    // add the partial tiles in wave order
+    __syncthreads();
+    float(*red)[MB][4][64] = reinterpret_cast<float(*)[MB][4][64]>(smem);
+#pragma unroll
+    for (int m = 0; m < MB; ++m)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) red[wave][m][i][lane] = acc[m][i];
+    __syncthreads();
+    for (int o = threadIdx.x; o < OUTS; o += WK * 64) {
+        const int l = o & 63, i = (o >> 6) & 3, m = o >> 8;
+        const int row = m * 16 + 4 * (l >> 4) + i, col = l & 15;
+        float v = red[0][m][i][l];
+        for (int w = 1; w < WK; ++w) v += red[w][m][i][l];
+        if (row < rows && col < cols) store_out(p.out, row0 + row, col0 + col, v);
+    }
+}
+
+template <int DT, int QT, int GROUP>
+static hipError_t launch_rows(const W4Params &p, hipStream_t s) {
+    const dim3 grid((p.N + 15) / 16, (p.M + 31) / 32);
+    if (grid.y > 65535) return hipErrorInvalidValue;
+    if (p.M <= 2) hipLaunchKernelGGL((gemm_w4_rows_kernel<DT, QT, GROUP, 2, 8, 4>), grid, dim3(512), 0, s, p);
+    else if (p.M <= 8) hipLaunchKernelGGL((gemm_w4_rows_kernel<DT, QT, GROUP, 8, 8, 2>), grid, dim3(512), 0, s, p);
+    else if (p.M <= 16) hipLaunchKernelGGL((gemm_w4_rows_kernel<DT, QT, GROUP, 16, 4, 3>), grid, dim3(256), 0, s, p);
+    else hipLaunchKernelGGL((gemm_w4_rows_kernel<DT, QT, GROUP, 32, 4, 2>), grid, dim3(256), 0, s, p);
+    return hipGetLastError();
+}
+template <int DT, int QT>
+static hipError_t by_group(const W4Params &p, hipStream_t s) {
+    switch (p.group) {
+    case 32: return launch_rows<DT, QT, 32>(p, s);
+    case 64: return launch_rows<DT, QT, 64>(p, s);
+    case 0:
+    case 128: return launch_rows<DT, QT, 128>(p, s);
+    default: return hipErrorInvalidValue;
+    }
+}
+
+hipError_t launch_gemm_w4(int a, int q, const W4Params &p, hipStream_t s) {
+    if (a == DT_BF16) return q == DT_FP4 ? by_group<DT_BF16, DT_FP4>(p, s) : by_group<DT_BF16, DT_U4>(p, s);
+    if (a == DT_F16) return q == DT_FP4 ? by_group<DT_F16, DT_FP4>(p, s) : by_group<DT_F16, DT_U4>(p, s);
+    return hipErrorInvalidValue;
+}
+
+}  // namespace mmac

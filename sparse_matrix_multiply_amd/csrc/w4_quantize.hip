@@ -1,0 +1,231 @@
+// Weights to 4 bits with a scale word per group of a row.
+//
+// Per group: the range r of its values, the scale s = r / steps (fp32, then 16
+// significant bits), the zero point z, and for each value the integer nearest to
+// w / s, ties to even, of the exact quotient.  An fp32 quotient is rounded, so a
+// value just off the middle between two integers could land on it: only there the
+// sign of the exact remainder w - q * s (one fused multiply-add rounds once and
+// keeps the sign) decides.
+//
+// The work is a streaming pass, bound by HBM.  Groups of 32 to 128: a lane
+// holds eight elements, 4 to 16 lanes a group, a wave 128 columns of 32 rows; the
+// scale words (group-major) are gathered in LDS so that a wave writes 32
+// consecutive ones at a time.  Whole rows: one workgroup per row reads the row
+// twice, the second time from the caches.
+#include <algorithm>
+
+#include "lowbit.h"
+
+namespace mmac {
+
+// The integer nearest to a / s (s > 0), ties to even, exact quotient.
+__device__ __forceinline__ float nearest_quotient(float a, float s) {
+    const float q = a / s, n = __builtin_rintf(q);
+    if (__builtin_fabsf(q - n) == 0.5f) {
+        const float rest = fmaf(-q, s, a);
+        if (rest > 0.0f) return __builtin_ceilf(q);
+        if (rest < 0.0f) return __builtin_floorf(q);
+    }
+    return n;
+}
+
+// Code of the E2M1 value nearest to a / s (a >= 0, s > 0), ties to the even code.
+__device__ __forceinline__ uint32_t nearest_e2m1(float a, float s) {
+    const float q = a / s;
+    constexpr float middle[7] = {0.25f, 0.75f, 1.25f, 1.75f, 2.5f, 3.5f, 5.0f};
+    uint32_t code = 0;
+#pragma unroll
+    for (int i = 0; i < 7; ++i) {
+        bool up = q > middle[i];
+        if (q == middle[i]) {
+            const float rest = fmaf(-q, s, a);
+            up = rest > 0.0f || (rest == 0.0f && (i & 1));
+        }
+        code += up;
+    }
+    return code;
+}
+
+// Range of a group's values, gathered over elements and lanes.
+struct Range {
+    float lo = 0.0f, hi = 0.0f;
+    uint32_t top = 0;   // bits of the largest magnitude; non-finite values are the largest
+    __device__ __forceinline__ void add(float x) {
+        lo = fminf(lo, x);
+        hi = fmaxf(hi, x);
+        top = max(top, __builtin_bit_cast(uint32_t, x) & 0x7fffffffu);
+    }
+};
+
+// The scale word's scale and zero point.
+template <int QT, bool SYM>
+__device__ __forceinline__ uint32_t scale_word(const Range &r, float &s, float &z) {
+    const float top = __builtin_bit_cast(float, r.top);
+    const float steps = QT == DT_FP4 ? 6.0f : SYM ? 7.0f : 15.0f;
+    s = (QT == DT_FP4 || SYM ? top : r.hi - r.lo) / steps;
+    z = QT == DT_FP4 ? 0.0f : SYM ? 8.0f : 0.0f;
+    uint32_t u = __builtin_bit_cast(uint32_t, s);
+    if (r.top >= 0x7f800000u || u >= 0x7f800000u) {      // a NaN, an infinity, or a range past fp32
+        s = 0.0f;
+        return 0x7fc00000u | (uint32_t)z;
+    }
+    if (u < 0x00800000u) {
+        s = 0.0f;
+        return (uint32_t)z;
+    }
+    u = (u + 0x7fu + ((u >> 8) & 1u)) & ~0xffu;
+    s = __builtin_bit_cast(float, u);
+    if (QT != DT_FP4 && !SYM) z = fminf(fmaxf(nearest_quotient(-r.lo, s), 0.0f), 15.0f);
+    return u | (uint32_t)z;
+}
+
+template <int QT>
+__device__ __forceinline__ uint32_t code_of(float x, float s, float z) {
+    if constexpr (QT == DT_FP4) {
+        if (s == 0.0f) return 0;
+        return nearest_e2m1(__builtin_fabsf(x), s) | (x < 0.0f ? 8u : 0u);
+    } else {
+        if (s == 0.0f) return (uint32_t)z;
+        return (uint32_t)fminf(fmaxf(nearest_quotient(x, s) + z, 0.0f), 15.0f);
+    }
+}
+
+// Eight codes of a lane's elements e0 .. e0 + 7, those at and past K zero.
+template <int QT>
+__device__ __forceinline__ uint32_t codes_of(const float (&x)[8], float s, float z, int e0, int K) {
+    uint32_t w = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (e0 + i < K) w |= code_of<QT>(x[i], s, z) << (4 * i);
+    return w;
+}
+
+constexpr int kRows = 32, kSteps = kRows / 4;
+
+template <int WT, int QT, bool SYM, int GROUP>
+__global__ __launch_bounds__(256) void w4_quantize_kernel(W4QuantParams p, int64_t units, int strips) {
+    constexpr int LANES = GROUP / 8, PER = 128 / GROUP;   // lanes of a group, groups of a strip
+    __shared__ uint32_t words[4][PER][kRows];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l16 = lane & 15, quarter = lane >> 4;
+    const int kp = (p.K + 31) / 32 * 32;
+    const int groups = (p.K + GROUP - 1) / GROUP;
+    for (int64_t unit = (int64_t)blockIdx.x * 4 + wave; unit < units; unit += (int64_t)gridDim.x * 4) {
+        const int strip = (int)(unit % strips);
+        const int64_t row0 = unit / strips * kRows;
+        const int e0 = strip * 128 + l16 * 8;
+        float x[kSteps][8];
+#pragma unroll
+        for (int st = 0; st < kSteps; ++st) {
+            const int64_t row = row0 + 4 * st + quarter;
+            load8<WT>(x[st], p.W + row * p.w_pitch, e0, row < p.N ? p.K : 0);
+        }
+#pragma unroll
+        for (int st = 0; st < kSteps; ++st) {
+            const int64_t row = row0 + 4 * st + quarter;
+            Range r;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) r.add(x[st][i]);
+            r.top = reduce_lanes<LANES>(r.top, [](uint32_t a, uint32_t b) { return max(a, b); });
+            if constexpr (QT != DT_FP4 && !SYM) {
+                const auto fmin_ = [](uint32_t a, uint32_t b) {
+                    return __builtin_bit_cast(uint32_t, fminf(__builtin_bit_cast(float, a), __builtin_bit_cast(float, b)));
+                };
+                const auto fmax_ = [](uint32_t a, uint32_t b) {
+                    return __builtin_bit_cast(uint32_t, fmaxf(__builtin_bit_cast(float, a), __builtin_bit_cast(float, b)));
+                };
+                r.lo = __builtin_bit_cast(float, reduce_lanes<LANES>(__builtin_bit_cast(uint32_t, r.lo), fmin_));
+                r.hi = __builtin_bit_cast(float, reduce_lanes<LANES>(__builtin_bit_cast(uint32_t, r.hi), fmax_));
+            }
+            float s, z;
+            const uint32_t word = scale_word<QT, SYM>(r, s, z);
+            const uint32_t q = codes_of<QT>(x[st], s, z, e0, p.K);
+            if (row < p.N && e0 < kp) *reinterpret_cast<uint32_t *>(p.codes + row * p.pitch + e0 / 2) = q;
+            if (l16 % LANES == 0) words[wave][l16 / LANES][4 * st + quarter] = word;
+        }
+        wave_sync();
+#pragma unroll
+        for (int j = 0; j < (PER + 1) / 2; ++j) {
+            const int g = 2 * j + lane / kRows, group = strip * PER + g;
+            const int64_t row = row0 + lane % kRows;
+            if (g < PER && group < groups && row < p.N) p.words[group * p.ldw + row] = words[wave][g][lane % kRows];
+        }
+        wave_sync();
+    }
+}
+
+template <int WT, int QT, bool SYM>
+__global__ __launch_bounds__(256) void w4_quantize_rows_kernel(W4QuantParams p) {
+    __shared__ float lo[4], hi[4];
+    __shared__ uint32_t top[4];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int kp = (p.K + 31) / 32 * 32;
+    for (int64_t row = blockIdx.x; row < p.N; row += gridDim.x) {
+        const uint8_t *src = p.W + row * p.w_pitch;
+        Range r;
+        for (int64_t e0 = threadIdx.x * 8; e0 < p.K; e0 += 256 * 8) {
+            float x[8];
+            load8<WT>(x, src, e0, p.K);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) r.add(x[i]);
+        }
+        for (int d = 1; d < 64; d *= 2) {
+            r.lo = fminf(r.lo, __shfl_xor(r.lo, d));
+            r.hi = fmaxf(r.hi, __shfl_xor(r.hi, d));
+            r.top = max(r.top, (uint32_t)__shfl_xor((int)r.top, d));
+        }
+        if (lane == 0) {
+            lo[wave] = r.lo;
+            hi[wave] = r.hi;
+            top[wave] = r.top;
+        }
+        __syncthreads();
+        for (int w = 0; w < 4; ++w) {
+            r.lo = fminf(r.lo, lo[w]);
+            r.hi = fmaxf(r.hi, hi[w]);
+            r.top = max(r.top, top[w]);
+        }
+        __syncthreads();   // before the next row's values
+        float s, z;
+        const uint32_t word = scale_word<QT, SYM>(r, s, z);
+        if (threadIdx.x == 0) p.words[row] = word;
+        for (int64_t e0 = threadIdx.x * 8; e0 < kp; e0 += 256 * 8) {
+            float x[8];
+            load8<WT>(x, src, e0, p.K);
+            *reinterpret_cast<uint32_t *>(p.codes + row * p.pitch + e0 / 2) = codes_of<QT>(x, s, z, (int)e0, p.K);
+        }
+    }
+}
+
+template <int WT, int QT, bool SYM>
+static hipError_t launch_as(int group, const W4QuantParams &p, hipStream_t s) {
+    if (group == 0) {
+        hipLaunchKernelGGL((w4_quantize_rows_kernel<WT, QT, SYM>), dim3((unsigned)std::min(p.N, 1 << 20)), dim3(256), 0, s, p);
+        return hipGetLastError();
+    }
+    const int strips = (p.K + 127) / 128;
+    const int64_t units = (int64_t)strips * ((p.N + kRows - 1) / kRows);
+    const dim3 grid((unsigned)std::min<int64_t>((units + 3) / 4, 1 << 20)), block(256);
+    switch (group) {
+    case 32: hipLaunchKernelGGL((w4_quantize_kernel<WT, QT, SYM, 32>), grid, block, 0, s, p, units, strips); break;
+    case 64: hipLaunchKernelGGL((w4_quantize_kernel<WT, QT, SYM, 64>), grid, block, 0, s, p, units, strips); break;
+    case 128: hipLaunchKernelGGL((w4_quantize_kernel<WT, QT, SYM, 128>), grid, block, 0, s, p, units, strips); break;
+    default: return hipErrorInvalidValue;
+    }
+    return hipGetLastError();
+}
+template <int WT>
+static hipError_t by_code(int q, bool sym, int group, const W4QuantParams &p, hipStream_t s) {
+    if (q == DT_FP4) return launch_as<WT, DT_FP4, true>(group, p, s);
+    return sym ? launch_as<WT, DT_U4, true>(group, p, s) : launch_as<WT, DT_U4, false>(group, p, s);
+}
+
+hipError_t launch_w4_quantize(int w, int q, bool sym, int group, const W4QuantParams &p, hipStream_t s) {
+    switch (w) {
+    case DT_F16: return by_code<DT_F16>(q, sym, group, p, s);
+    case DT_BF16: return by_code<DT_BF16>(q, sym, group, p, s);
+    case DT_F32: return by_code<DT_F32>(q, sym, group, p, s);
+    default: return hipErrorInvalidValue;
+    }
+}
+
+}  // namespace mmac
