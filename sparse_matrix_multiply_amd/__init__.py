@@ -392,13 +392,42 @@ def gemm_layout(A, B, D, trans_a=False, trans_b=False, alpha=1.0, beta=0.0, C=No
 
 
 # ---- low-bit operands (include/mmac_lowbit.h) ----------------------------------------------------
+# A product for one token takes a few microseconds, as long as a call takes on the host: the checks
+# below look at every tensor once, and pass addresses as plain integers.
 
-def _current_device(*tensors):
-    """Every tensor lives on the current CUDA device, the one the call's stream belongs to."""
-    _same_device(*tensors)
+def _rows_of(t, rows, cols, name, wider=False):
+    """_shape and _ld in one: checks a 2-D tensor and returns its row pitch in elements."""
+    sh = t.shape
+    if len(sh) != 2 or sh[0] != rows or (sh[1] < cols if wider else sh[1] != cols):
+        raise ValueError(f"{name} has shape {tuple(sh)}, expected ({rows}, {'>= ' if wider else ''}{cols})")
+    pitch, step = t.stride()
+    width = sh[1]
+    if step != 1 and width > 1:
+        raise ValueError(f"{name}: expected a contiguous last dimension")
+    if pitch < width:
+        if rows > 1:
+            raise ValueError(f"{name}: rows of a {tuple(sh)} tensor with row stride {pitch} overlap")
+        pitch = width
+    return pitch if pitch > 0 else 1
+
+
+def _stream_of(stream, *tensors):
+    """The stream of a call, whose tensors must all live on the current CUDA device, the one it belongs to."""
+    device = tensors[0].get_device()
     for t in tensors:
-        if t is not None and t.device.index != torch.cuda.current_device():
-            raise ValueError(f"tensors on {t.device}, but the current device is cuda:{torch.cuda.current_device()}")
+        if t is not None and t.get_device() != device:
+            raise ValueError(f"tensors on different devices: {sorted({str(x.device) for x in tensors if x is not None})}")
+    if device < 0:
+        raise ValueError("every tensor must be in GPU memory")
+    if device != torch._C._cuda_getDevice():
+        raise ValueError(f"tensors on cuda:{device}, but the current device is cuda:{torch.cuda.current_device()}")
+    if stream is not None:
+        if stream.device_index != device:
+            raise ValueError(f"tensors on cuda:{device}, the stream on cuda:{stream.device_index}")
+        return stream.cuda_stream
+    if _raw_current_stream is not None:
+        return _raw_current_stream(device)
+    return torch.cuda.current_stream().cuda_stream
 
 
 def _input_type(t, given):
@@ -407,20 +436,38 @@ def _input_type(t, given):
         if t.element_size() != {F32: 4, F16: 2, BF16: 2}.get(given, t.element_size()):
             raise ValueError(f"a tensor of {t.element_size()}-byte elements for type code {given}")
         return given
-    if t.dtype not in (torch.float16, torch.bfloat16, torch.float32):
+    code = _INPUT_OF.get(t.dtype)
+    if code is None:
         raise ValueError(f"expected a float16, bfloat16 or float32 tensor, got {t.dtype}")
-    return F32 if t.dtype == torch.float32 else DTYPE_OF[t.dtype]
+    return code
+
+
+_INPUT_OF = {torch.float16: F16, torch.bfloat16: BF16, torch.float32: F32}
+# dtypes of codes and elements, and of scale words
+_BYTES = {torch.uint8, torch.int8, torch.float8_e4m3fn, torch.float8_e5m2}
+_WORDS = {torch.int32, torch.uint32}
 
 
 def _w4(Wq, SW, N, K, group, q_type):
     """The mmac_w4_t of a weight matrix."""
-    _shape(Wq, N, (K + 31) // 32 * 16, "Wq", min_cols=True)
-    if Wq.element_size() != 1:
+    if Wq.dtype not in _BYTES:
         raise ValueError("Wq must hold bytes, two codes each")
-    if SW.element_size() != 4:
+    if SW.dtype not in _WORDS:
         raise ValueError("SW must hold 32-bit scale words")
-    _shape(SW, 1 if group == 0 else (K + group - 1) // group, N, "SW", min_cols=True)
-    return W4(q_type, group, Wq.data_ptr(), max(_ld(Wq), 16), SW.data_ptr(), _ld(SW))
+    pitch = _rows_of(Wq, N, (K + 31) // 32 * 16, "Wq", True)
+    ldw = _rows_of(SW, (K + group - 1) // group if group > 0 else 1, N, "SW", True)
+    return W4(q_type, group, Wq.data_ptr(), pitch if pitch > 16 else 16, SW.data_ptr(), ldw)
+
+
+def _mx8(Xq, SX, M, K, q_type):
+    """Checks an mx8 matrix; returns its element type's code and both pitches."""
+    if q_type is None:
+        q_type = DTYPE_OF.get(Xq.dtype)
+    if Xq.dtype not in _BYTES or q_type is None:
+        raise ValueError(f"Xq must hold float8_e4m3fn, float8_e5m2 or int8 elements, got {Xq.dtype}")
+    if SX.dtype not in _WORDS:
+        raise ValueError("SX must hold 32-bit scale words")
+    return (q_type, _rows_of(Xq, M, (K + 31) // 32 * 32, "Xq", True), _rows_of(SX, (K + 127) // 128, M, "SX", True))
 
 
 def _workspace_tensor(nbytes, device):
@@ -430,7 +477,11 @@ def _workspace_tensor(nbytes, device):
 
 
 def _workspace_args(workspace):
-    return (None, 0) if workspace is None else (_ptr(workspace), workspace.numel() * workspace.element_size())
+    if workspace is None:
+        return None, 0
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def w4_quantize(W, Wq, SW, group=128, q_type=U4, symmetric=False, w_type=None, stream=None):
@@ -439,9 +490,9 @@ def w4_quantize(W, Wq, SW, group=128, q_type=U4, symmetric=False, w_type=None, s
     row, rounded to nearest.  q_type U4 (symmetric: zero point 8) or FP4_E2M1 (symmetric)."""
     N, K = W.shape
     q = _w4(Wq, SW, N, K, group, q_type)
-    _current_device(W, Wq, SW)
-    _check(lib().mmac_w4_quantize(_input_type(W, w_type), int(bool(symmetric or q_type == FP4_E2M1)), N, K, _ptr(W),
-                                  _ld(W), ctypes.byref(q), _stream(stream)), "mmac_w4_quantize")
+    _check(lib().mmac_w4_quantize(_input_type(W, w_type), 1 if symmetric or q_type == FP4_E2M1 else 0, N, K,
+                                  W.data_ptr(), _rows_of(W, N, K, "W"), ctypes.byref(q), _stream_of(stream, W, Wq, SW)),
+           "mmac_w4_quantize")
     return Wq, SW
 
 
@@ -462,28 +513,18 @@ def gemm_w4(A, Wq, SW, D, group=128, q_type=U4, alpha=1.0, beta=0.0, C=None, a_t
     K may be split."""
     M, K = A.shape
     N = Wq.shape[0]
-    _shape(D, M, N, "D")
-    _shape(C, M, N, "C")
-    _bias(bias, N)
-    _current_device(A, Wq, SW, C, D, bias, workspace)
+    ldd = _rows_of(D, M, N, "D")
+    ldc = _rows_of(C, M, N, "C") if C is not None else 0
+    if bias is not None:
+        _bias(bias, N)
     q = _w4(Wq, SW, N, K, group, q_type)
     ep = _epilogue(D, bias, act, d_type, C)
-    _check(lib().mmac_gemm_w4(_input_type(A, a_type), M, N, K, float(alpha), _ptr(A), _ld(A), ctypes.byref(q),
-                              float(beta), _ptr(C), _ld(C) if C is not None else 0, _ptr(D), _ld(D),
-                              None if ep is None else ctypes.byref(ep), *_workspace_args(workspace), _stream(stream)),
-           "mmac_gemm_w4")
+    ws, nbytes = _workspace_args(workspace)
+    _check(lib().mmac_gemm_w4(_input_type(A, a_type), M, N, K, alpha, A.data_ptr(), _rows_of(A, M, K, "A"),
+                              ctypes.byref(q), beta, C.data_ptr() if C is not None else None, ldc, D.data_ptr(), ldd,
+                              None if ep is None else ctypes.byref(ep), ws, nbytes,
+                              _stream_of(stream, A, Wq, SW, C, D, bias, workspace)), "mmac_gemm_w4")
     return D
-
-
-def _mx8(Xq, SX, M, K, q_type):
-    """Checks an mx8 matrix; returns its element type's code."""
-    _shape(Xq, M, (K + 31) // 32 * 32, "Xq", min_cols=True)
-    if Xq.element_size() != 1 or (q_type is None and Xq.dtype not in DTYPE_OF):
-        raise ValueError(f"Xq must hold float8_e4m3fn, float8_e5m2 or int8 elements, got {Xq.dtype}")
-    if SX.element_size() != 4:
-        raise ValueError("SX must hold 32-bit scale words")
-    _shape(SX, (K + 127) // 128, M, "SX", min_cols=True)
-    return _dtype(Xq, q_type)
 
 
 def mx8_quantize(X, Xq, SX, x_type=None, q_type=None, stream=None):
@@ -491,20 +532,19 @@ def mx8_quantize(X, Xq, SX, x_type=None, q_type=None, stream=None):
     float8_e4m3fn, float8_e5m2 or int8) and scale words SX (ceil(K/128) x M int32): the operand
     form of gemm_mx, and of gemm_mx8_wgrad."""
     M, K = X.shape
-    tq = _mx8(Xq, SX, M, K, q_type)
-    _current_device(X, Xq, SX)
-    _check(lib().mmac_mx8_quantize(_input_type(X, x_type), tq, M, K, _ptr(X), _ld(X), _ptr(Xq), _ld(Xq),
-                                   _ptr(SX), _ld(SX), _stream(stream)), "mmac_mx8_quantize")
+    tq, ldq, lds = _mx8(Xq, SX, M, K, q_type)
+    _check(lib().mmac_mx8_quantize(_input_type(X, x_type), tq, M, K, X.data_ptr(), _rows_of(X, M, K, "X"), Xq.data_ptr(),
+                                   ldq, SX.data_ptr(), lds, _stream_of(stream, X, Xq, SX)), "mmac_mx8_quantize")
     return Xq, SX
 
 
 def mx8_dequantize(Xq, SX, X, q_type=None, x_type=None, stream=None):
     """The activations that (Xq, SX) stand for, rounded to X's type; X gives M and K."""
     M, K = X.shape
-    tq = _mx8(Xq, SX, M, K, q_type)
-    _current_device(X, Xq, SX)
-    _check(lib().mmac_mx8_dequantize(tq, _input_type(X, x_type), M, K, _ptr(Xq), _ld(Xq), _ptr(SX),
-                                     _ld(SX), _ptr(X), _ld(X), _stream(stream)), "mmac_mx8_dequantize")
+    tq, ldq, lds = _mx8(Xq, SX, M, K, q_type)
+    _check(lib().mmac_mx8_dequantize(tq, _input_type(X, x_type), M, K, Xq.data_ptr(), ldq, SX.data_ptr(), lds,
+                                     X.data_ptr(), _rows_of(X, M, K, "X"), _stream_of(stream, X, Xq, SX)),
+           "mmac_mx8_dequantize")
     return X
 
 
@@ -524,16 +564,16 @@ def gemm_mx8_wgrad(dY, Xq, SX, D, alpha=1.0, beta=0.0, C=None, y_type=None, q_ty
     linear layer's output and its input as mx8_quantize stored it; D gives K."""
     M, N = dY.shape
     K = D.shape[1]
-    tq = _mx8(Xq, SX, M, K, q_type)
-    _shape(D, N, K, "D")
-    _shape(C, N, K, "C")
-    _current_device(dY, Xq, SX, C, D, workspace)
+    ldd = _rows_of(D, N, K, "D")
+    ldc = _rows_of(C, N, K, "C") if C is not None else 0
+    tq, ldq, lds = _mx8(Xq, SX, M, K, q_type)
     ep = _epilogue(D, None, ACT_NONE, d_type, C)
-    _check(lib().mmac_gemm_mx8_wgrad(_input_type(dY, y_type), tq, M, N, K, float(alpha), _ptr(dY),
-                                     _ld(dY), _ptr(Xq), _ld(Xq), _ptr(SX), _ld(SX), float(beta), _ptr(C),
-                                     _ld(C) if C is not None else 0, _ptr(D), _ld(D),
-                                     None if ep is None else ctypes.byref(ep), *_workspace_args(workspace),
-                                     _stream(stream)), "mmac_gemm_mx8_wgrad")
+    ws, nbytes = _workspace_args(workspace)
+    _check(lib().mmac_gemm_mx8_wgrad(_input_type(dY, y_type), tq, M, N, K, alpha, dY.data_ptr(),
+                                     _rows_of(dY, M, N, "dY"), Xq.data_ptr(), ldq, SX.data_ptr(), lds, beta,
+                                     C.data_ptr() if C is not None else None, ldc, D.data_ptr(), ldd,
+                                     None if ep is None else ctypes.byref(ep), ws, nbytes,
+                                     _stream_of(stream, dY, Xq, SX, C, D, workspace)), "mmac_gemm_mx8_wgrad")
     return D
 
 

@@ -113,6 +113,15 @@ SplitParams apply(const SplitPlan &s, int64_t chunks, void *ws, int64_t ws_bytes
     return SplitParams{s.splits, s.per_split, static_cast<uint32_t *>(ws), static_cast<uint8_t *>(ws) + s.counter_bytes};
 }
 
+// 4-bit products of more than 32 rows: tiles of K ranges when the tiles alone leave compute units idle, each
+// range at least two chunks.
+SplitPlan plan_w4(int64_t M, int64_t N, int64_t K) {
+    if (M <= 32 || N == 0 || K == 0) return SplitPlan{1, 1, 0, 0};
+    const int64_t bm = w4_tile_rows(M), tiles = ((M + bm - 1) / bm) * ((N + kW4Cols - 1) / kW4Cols);
+    const int64_t chunks = (K + kW4Chunk - 1) / kW4Chunk;
+    return plan(tiles, bm * kW4Cols * 4, chunks, std::min<int64_t>({16, 256 / tiles, chunks / 2}));
+}
+
 // Weight gradient: two workgroups per compute unit (512) by cutting M into at most 16 ranges of at least
 // four chunks.
 SplitPlan plan_wgrad(int64_t M, int64_t N, int64_t K) {
@@ -178,13 +187,18 @@ mmac_status_t mmac_gemm_w4(mmac_dtype_t a_type, int64_t M, int64_t N, int64_t K,
     p.N = (int)N;
     p.K = (int)K;
     p.out = out_params(alpha, beta, C, ldc, D, ldd, ep);
-    p.split = SplitParams{1, 0x7fffffff, nullptr, nullptr};
-    return launched(launch_gemm_w4(a_type, W->q_type, p, static_cast<hipStream_t>(stream)));
+    if (M <= 32) return launched(launch_gemm_w4_rows(a_type, W->q_type, p, static_cast<hipStream_t>(stream)));
+    const int64_t bm = w4_tile_rows(M), tm = (M + bm - 1) / bm, tn = (N + kW4Cols - 1) / kW4Cols;
+    if (tm * tn > INT32_MAX / 1024) return MMAC_ERR_UNSUPPORTED;   // the grid, up to 512 threads each
+    p.tiles_m = (int)tm;
+    p.tiles_n = (int)tn;
+    p.split = apply(plan_w4(M, N, K), (K + kW4Chunk - 1) / kW4Chunk, workspace, workspace_bytes);
+    return launched(launch_gemm_w4_tiled(a_type, W->q_type, p, static_cast<hipStream_t>(stream)));
 }
 
 int64_t mmac_gemm_w4_workspace_bytes(int64_t M, int64_t N, int64_t K) {
-    (void)M; (void)N; (void)K;
-    return 0;
+    if (bad_dim(M) || bad_dim(N) || bad_dim(K)) return 0;
+    return plan_w4(M, N, K).bytes;
 }
 
 static mmac_status_t check_mx8(int x_type, int q_type, int64_t M, int64_t K, const void *X, int64_t ldx, const void *Xq,

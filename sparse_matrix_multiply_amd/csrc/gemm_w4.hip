@@ -8,11 +8,6 @@
 // accumulator starts at zero in every group, a second one sums A itself (an
 // operand of ones), and at the group's end s * (t - z * u) joins the fp32 total.
 //
-// Codes to 16-bit operands: the byte 0x0n read as E4M3 is n * 2^-9 for every n
-// from 0 to 15 (subnormals up to 7, then the first normal binade), so the
-// instructions that convert pairs of fp8 values with a power-of-two scale give n
-// exactly; E2M1 codes have a conversion of their own.
-//
 // A workgroup owns 16 columns of D and all rows (up to 32); its WK waves split K
 // into contiguous ranges of chunks of 256 elements: of a weight row one 128-byte
 // line, of A 512 bytes.  Each wave copies its chunks straight into a private ring
@@ -20,44 +15,9 @@
 // from there; no barrier until the partial tiles are added up in wave order.  The
 // time is that of streaming the codes from HBM.
 #include "gemm_tiled.h"
-#include "lowbit.h"
+#include "w4_operand.h"
 
 namespace mmac {
-
-// Eight codes of a word, ascending, as a 16-byte operand of DT values.
-template <int DT, int QT>
-__device__ __forceinline__ i32x4 operand_of(uint32_t w) {
-    i32x4 f;
-    if constexpr (QT == DT_FP4) {
-        if constexpr (DT == DT_BF16) {
-            f[0] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.0f, 0));
-            f[1] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.0f, 1));
-            f[2] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.0f, 2));
-            f[3] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.0f, 3));
-        } else {
-            f[0] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 0));
-            f[1] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 1));
-            f[2] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 2));
-            f[3] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 3));
-        }
-    } else {
-        const uint32_t even = w & 0x0f0f0f0fu, odd = (w >> 4) & 0x0f0f0f0fu;
-        // bytes in ascending order: n0 n1 n2 n3 and n4 n5 n6 n7
-        const uint32_t p0 = __builtin_amdgcn_perm(odd, even, 0x05010400u), p1 = __builtin_amdgcn_perm(odd, even, 0x07030602u);
-        if constexpr (DT == DT_BF16) {
-            f[0] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(p0, 512.0f, false));
-            f[1] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(p0, 512.0f, true));
-            f[2] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(p1, 512.0f, false));
-            f[3] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(p1, 512.0f, true));
-        } else {
-            f[0] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(p0, 512.0f, false));
-            f[1] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(p0, 512.0f, true));
-            f[2] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(p1, 512.0f, false));
-            f[3] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(p1, 512.0f, true));
-        }
-    }
-    return f;
-}
 
 template <int DT>
 __device__ __forceinline__ f32x4 mma16(const i32x4 &a, const i32x4 &b, f32x4 c) {
@@ -84,11 +44,11 @@ __global__ __launch_bounds__(WK * 64) void gemm_w4_rows_kernel(W4Params p) {
     static_assert(LDS_BYTES <= 160 * 1024 && (NSLOT - 1) * IPC < 64, "LDS and counter range");
     __shared__ __attribute__((aligned(16))) uint8_t smem[LDS_BYTES];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r16 = lane & 15, q = lane >> 4;
-    const int col0 = blockIdx.x * 16, row0 = blockIdx.y * 32;
-    const int rows = min(p.M - row0, MR), cols = min(16, p.N - col0);
+    const int col0 = blockIdx.x * 16, rows = p.M;
+    const int cols = min(16, p.N - col0);
     const int row_bytes = (p.K + 31) / 32 * 16;
-    const rsrc_t ra = make_rsrc(p.A + row0 * p.a_pitch, (uint32_t)(rows * p.a_pitch));
-    const rsrc_t rw = make_rsrc(p.codes + col0 * p.pitch, (uint32_t)((cols - 1) * p.pitch + row_bytes));
+    const rsrc_t ra = make_rsrc(p.A, (uint32_t)(rows * p.a_pitch));
+    const rsrc_t rw = make_rsrc(p.codes + (int64_t)col0 * p.pitch, (uint32_t)((cols - 1) * p.pitch + row_bytes));
     const rsrc_t rs = make_rsrc(p.words + col0, (uint32_t)(((p.groups - 1) * p.ldw + cols) * 4));
 
     f32x4 acc[MB];
@@ -214,14 +174,13 @@ __global__ __launch_bounds__(WK * 64) void gemm_w4_rows_kernel(W4Params p) {
         const int row = m * 16 + 4 * (l >> 4) + i, col = l & 15;
         float v = red[0][m][i][l];
         for (int w = 1; w < WK; ++w) v += red[w][m][i][l];
-        if (row < rows && col < cols) store_out(p.out, row0 + row, col0 + col, v);
+        if (row < rows && col < cols) store_out(p.out, row, col0 + col, v);
     }
 }
 
 template <int DT, int QT, int GROUP>
 static hipError_t launch_rows(const W4Params &p, hipStream_t s) {
-    const dim3 grid((p.N + 15) / 16, (p.M + 31) / 32);
-    if (grid.y > 65535) return hipErrorInvalidValue;
+    const dim3 grid((p.N + 15) / 16);
     if (p.M <= 2) hipLaunchKernelGGL((gemm_w4_rows_kernel<DT, QT, GROUP, 2, 8, 4>), grid, dim3(512), 0, s, p);
     else if (p.M <= 8) hipLaunchKernelGGL((gemm_w4_rows_kernel<DT, QT, GROUP, 8, 8, 2>), grid, dim3(512), 0, s, p);
     else if (p.M <= 16) hipLaunchKernelGGL((gemm_w4_rows_kernel<DT, QT, GROUP, 16, 4, 3>), grid, dim3(256), 0, s, p);
@@ -239,7 +198,7 @@ static hipError_t by_group(const W4Params &p, hipStream_t s) {
     }
 }
 
-hipError_t launch_gemm_w4(int a, int q, const W4Params &p, hipStream_t s) {
+hipError_t launch_gemm_w4_rows(int a, int q, const W4Params &p, hipStream_t s) {
     if (a == DT_BF16) return q == DT_FP4 ? by_group<DT_BF16, DT_FP4>(p, s) : by_group<DT_BF16, DT_U4>(p, s);
     if (a == DT_F16) return q == DT_FP4 ? by_group<DT_F16, DT_FP4>(p, s) : by_group<DT_F16, DT_U4>(p, s);
     return hipErrorInvalidValue;

@@ -42,6 +42,7 @@ struct W4Params {
     int groups;          // scale words of a row
     int group;           // 32, 64, 128 or 0 (whole rows)
     int M, N, K;
+    int tiles_m, tiles_n;   // tiled kernel
     OutParams out;
     SplitParams split;
 };
@@ -79,12 +80,17 @@ struct WgradParams {
     SplitParams split;
 };
 
+// Geometry of the tiled 4-bit product: tile rows for M, tile columns, elements of K per chunk.
+inline int w4_tile_rows(int64_t M) { return M <= 64 ? 64 : 128; }
+constexpr int kW4Cols = 256, kW4Chunk = 128;
+
 // Geometry of the weight-gradient kernel: tile rows for N, tile columns, rows of M per chunk.
 inline int wgrad_rows(int64_t N) { return N <= 32 ? 32 : N <= 64 ? 64 : 128; }
 constexpr int kWgradCols = 128, kWgradChunk = 64;
 
 hipError_t launch_w4_quantize(int w_type, int q_type, bool symmetric, int group, const W4QuantParams &p, hipStream_t s);
-hipError_t launch_gemm_w4(int a_type, int q_type, const W4Params &p, hipStream_t s);
+hipError_t launch_gemm_w4_rows(int a_type, int q_type, const W4Params &p, hipStream_t s);
+hipError_t launch_gemm_w4_tiled(int a_type, int q_type, const W4Params &p, hipStream_t s);
 hipError_t launch_mx8_quantize(int x_type, int q_type, const Mx8Params &p, hipStream_t s);
 hipError_t launch_mx8_dequantize(int q_type, int x_type, const Mx8Params &p, hipStream_t s);
 hipError_t launch_gemm_mx8_wgrad(int y_type, int q_type, const WgradParams &p, hipStream_t s);
