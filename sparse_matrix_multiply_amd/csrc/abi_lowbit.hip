@@ -113,13 +113,19 @@ SplitParams apply(const SplitPlan &s, int64_t chunks, void *ws, int64_t ws_bytes
     return SplitParams{s.splits, s.per_split, static_cast<uint32_t *>(ws), static_cast<uint8_t *>(ws) + s.counter_bytes};
 }
 
-// 4-bit products of more than 32 rows: tiles of K ranges when the tiles alone leave compute units idle, each
-// range at least two chunks.
+// 4-bit products of more than 32 rows: the largest tile that still gives a workgroup to most of the 256 compute
+// units; then, if tiles of 128 columns leave units idle, K ranges of at least two chunks.
+W4Tile w4_tile(int64_t M, int64_t N) {
+    const auto tiles = [&](W4Tile t) { return ((M + w4_rows(t) - 1) / w4_rows(t)) * ((N + w4_cols(t) - 1) / w4_cols(t)); };
+    if (M <= 64) return W4_64x128;
+    return tiles(W4_128x256) >= 192 ? W4_128x256 : W4_128x128;
+}
 SplitPlan plan_w4(int64_t M, int64_t N, int64_t K) {
     if (M <= 32 || N == 0 || K == 0) return SplitPlan{1, 1, 0, 0};
-    const int64_t bm = w4_tile_rows(M), tiles = ((M + bm - 1) / bm) * ((N + kW4Cols - 1) / kW4Cols);
+    const W4Tile t = w4_tile(M, N);
+    const int64_t tiles = ((M + w4_rows(t) - 1) / w4_rows(t)) * ((N + w4_cols(t) - 1) / w4_cols(t));
     const int64_t chunks = (K + kW4Chunk - 1) / kW4Chunk;
-    return plan(tiles, bm * kW4Cols * 4, chunks, std::min<int64_t>({16, 256 / tiles, chunks / 2}));
+    return plan(tiles, w4_rows(t) * w4_cols(t) * 4, chunks, std::min<int64_t>({8, 256 / tiles, chunks / 2}));
 }
 
 // Weight gradient: two workgroups per compute unit (512) by cutting M into at most 16 ranges of at least
@@ -188,7 +194,9 @@ mmac_status_t mmac_gemm_w4(mmac_dtype_t a_type, int64_t M, int64_t N, int64_t K,
     p.K = (int)K;
     p.out = out_params(alpha, beta, C, ldc, D, ldd, ep);
     if (M <= 32) return launched(launch_gemm_w4_rows(a_type, W->q_type, p, static_cast<hipStream_t>(stream)));
-    const int64_t bm = w4_tile_rows(M), tm = (M + bm - 1) / bm, tn = (N + kW4Cols - 1) / kW4Cols;
+    p.tile = w4_tile(M, N);
+
+    const int64_t tm = (M + w4_rows(p.tile) - 1) / w4_rows(p.tile), tn = (N + w4_cols(p.tile) - 1) / w4_cols(p.tile);
     if (tm * tn > INT32_MAX / 1024) return MMAC_ERR_UNSUPPORTED;   // the grid, up to 512 threads each
     p.tiles_m = (int)tm;
     p.tiles_n = (int)tn;

@@ -32,6 +32,12 @@ struct SplitParams {
     uint8_t *partials;
 };
 
+// Tiles of the 4-bit product for many rows, and elements of K per chunk.
+enum W4Tile : int { W4_128x256, W4_128x128, W4_64x128 };
+inline int w4_rows(W4Tile t) { return t == W4_64x128 ? 64 : 128; }
+inline int w4_cols(W4Tile t) { return t == W4_128x256 ? 256 : 128; }
+constexpr int kW4Chunk = 128;
+
 struct W4Params {
     const uint8_t *A;
     int64_t a_pitch;     // bytes
@@ -42,7 +48,8 @@ struct W4Params {
     int groups;          // scale words of a row
     int group;           // 32, 64, 128 or 0 (whole rows)
     int M, N, K;
-    int tiles_m, tiles_n;   // tiled kernel
+    W4Tile tile;            // tiled kernel
+    int tiles_m, tiles_n;
     OutParams out;
     SplitParams split;
 };
@@ -79,10 +86,6 @@ struct WgradParams {
     OutParams out;
     SplitParams split;
 };
-
-// Geometry of the tiled 4-bit product: tile rows for M, tile columns, elements of K per chunk.
-inline int w4_tile_rows(int64_t M) { return M <= 64 ? 64 : 128; }
-constexpr int kW4Cols = 256, kW4Chunk = 128;
 
 // Geometry of the weight-gradient kernel: tile rows for N, tile columns, rows of M per chunk.
 inline int wgrad_rows(int64_t N) { return N <= 32 ? 32 : N <= 64 ? 64 : 128; }
@@ -190,6 +193,44 @@ __device__ __forceinline__ void store_out(const OutParams &o, int64_t i, int64_t
             if (o.use_c) v = fmaf(o.beta, from_out_bits<OUT_E5M2>(*c), v);
             *d = (uint8_t)finish<OUT_E5M2>(v, bias, has_bias, relu);
         }
+    }
+}
+
+// A 32 x 32 accumulator tile to rows row0 .. row0 + 31 and column j of D (lane L: column L mod 32, register e: row
+// 8 (e / 4) + 4 (L / 32) + e mod 4); rows at and past `rows` and lanes with `in` false are left out.  All of C
+// is read before D is written, so that its 16 reads are in flight together (C may be D).
+template <int OT>
+__device__ __forceinline__ void store_tile_as(const OutParams &o, int64_t row0, int rows, int64_t j, bool in, const f32x16 &acc) {
+    typedef std::conditional_t<OT == OUT_ACC, uint32_t, std::conditional_t<OT <= OUT_F16, uint16_t, uint8_t>> T;
+    const int first = (threadIdx.x & 32) / 8;
+    const bool has_bias = o.bias != nullptr, relu = o.act != 0;
+    if (!in) return;
+    const float bias = has_bias ? o.bias[j] : 0.0f;
+    T c[16] = {};
+    if (o.use_c) {
+        const T *C = static_cast<const T *>(o.C) + row0 * o.ldc + j;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+            const int r = first + 8 * (e / 4) + e % 4;
+            if (r < rows) c[e] = C[r * o.ldc];
+        }
+    }
+    T *D = static_cast<T *>(o.D) + row0 * o.ldd + j;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+        const int r = first + 8 * (e / 4) + e % 4;
+        float v = o.alpha * acc[e];
+        if (o.use_c) v = fmaf(o.beta, from_out_bits<OT>(c[e]), v);
+        if (r < rows) D[r * o.ldd] = (T)finish<OT>(v, bias, has_bias, relu);
+    }
+}
+__device__ __forceinline__ void store_tile(const OutParams &o, int64_t row0, int rows, int64_t j, bool in, const f32x16 &acc) {
+    switch (o.d_type) {
+    case OUT_ACC: return store_tile_as<OUT_ACC>(o, row0, rows, j, in, acc);
+    case OUT_BF16: return store_tile_as<OUT_BF16>(o, row0, rows, j, in, acc);
+    case OUT_F16: return store_tile_as<OUT_F16>(o, row0, rows, j, in, acc);
+    case OUT_E4M3: return store_tile_as<OUT_E4M3>(o, row0, rows, j, in, acc);
+    default: return store_tile_as<OUT_E5M2>(o, row0, rows, j, in, acc);
     }
 }
 

@@ -232,13 +232,10 @@ __global__ __launch_bounds__(256) void gemm_mx8_wgrad_kernel(WgradParams p) {
 #pragma unroll
     for (int i = 0; i < TN; ++i)
 #pragma unroll
-        for (int j = 0; j < TK; ++j)
-#pragma unroll
-            for (int G = 0; G < 16; ++G) {
-                const int n = n0 + (wn * TN + i) * 32 + 8 * (G / 4) + 4 * (lane >> 5) + G % 4;
-                const int k = k0 + (wk * TK + j) * 32 + (lane & 31);
-                if (n < p.N && k < p.K) store_out(p.out, n, k, acc[i][j][G]);
-            }
+        for (int j = 0; j < TK; ++j) {
+            const int n = n0 + (wn * TN + i) * 32, k = k0 + (wk * TK + j) * 32 + (lane & 31);
+            store_tile(p.out, n, p.N - n, k, k < p.K, acc[i][j]);
+        }
 }
 
 template <int DT, int QT>
