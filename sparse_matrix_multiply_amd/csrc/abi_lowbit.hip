@@ -128,13 +128,20 @@ SplitPlan plan_w4(int64_t M, int64_t N, int64_t K) {
     return plan(tiles, w4_rows(t) * w4_cols(t) * 4, chunks, std::min<int64_t>({8, 256 / tiles, chunks / 2}));
 }
 
-// Weight gradient: two workgroups per compute unit (512) by cutting M into at most 16 ranges of at least
-// four chunks.
+// Weight gradient: 256 x 256 tiles where they occupy most compute units, else narrower ones (two or more workgroups
+// fit a unit) with M cut into ranges of at least four chunks until there are two workgroups per unit.
+WgradTile wgrad_tile(int64_t N, int64_t K) {
+    if (N <= 32) return WGRAD_32x128;
+    if (N <= 64) return WGRAD_64x128;
+    return ((N + 255) / 256) * ((K + 255) / 256) >= 192 ? WGRAD_256x256 : WGRAD_128x128;
+}
 SplitPlan plan_wgrad(int64_t M, int64_t N, int64_t K) {
     if (M == 0 || N == 0 || K == 0) return SplitPlan{1, 1, 0, 0};
-    const int64_t bn = wgrad_rows(N), tiles = ((N + bn - 1) / bn) * ((K + kWgradCols - 1) / kWgradCols);
+    const WgradTile t = wgrad_tile(N, K);
+    if (t == WGRAD_256x256) return SplitPlan{1, 1, 0, 0};
+    const int64_t tiles = ((N + wgrad_rows(t) - 1) / wgrad_rows(t)) * ((K + wgrad_cols(t) - 1) / wgrad_cols(t));
     const int64_t chunks = (M + kWgradChunk - 1) / kWgradChunk;
-    return plan(tiles, bn * kWgradCols * 4, chunks, std::min<int64_t>({16, 512 / tiles, chunks / 4}));
+    return plan(tiles, wgrad_rows(t) * wgrad_cols(t) * 4, chunks, std::min<int64_t>({16, 512 / tiles, chunks / 4}));
 }
 
 }  // namespace
@@ -278,7 +285,8 @@ mmac_status_t mmac_gemm_mx8_wgrad(mmac_dtype_t y_type, mmac_dtype_t q_type, int6
     p.M = (int)M;
     p.N = (int)N;
     p.K = (int)K;
-    const int64_t bn = wgrad_rows(N), tn = (N + bn - 1) / bn, tk = (K + kWgradCols - 1) / kWgradCols;
+    p.tile = wgrad_tile(N, K);
+    const int64_t bn = wgrad_rows(p.tile), bk = wgrad_cols(p.tile), tn = (N + bn - 1) / bn, tk = (K + bk - 1) / bk;
     if (tn * tk > INT32_MAX / 1024) return MMAC_ERR_UNSUPPORTED;   // the grid, 256 threads each and up to 16 ranges
     p.tiles_n = (int)tn;
     p.tiles_k = (int)tk;

@@ -70,12 +70,12 @@ void gemm_w4_tiled_kernel(W4Params p) {
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int g2 = lane >> 5, l32 = lane & 31, wm = wave / WN, wn = wave % WN;
 
-    // workgroup -> (tile, range): contiguous runs per XCD, then groups of 8 tile rows column by column
+    // workgroup -> (tile, range): contiguous runs per XCD, then groups of 4 tile rows column by column
     const int U = p.tiles_m * p.tiles_n * p.split.splits;
     const int x = blockIdx.x & 7, uq = U >> 3, ur = U & 7;
     const int unit = x * uq + (x < ur ? x : ur) + (blockIdx.x >> 3);
     const int tile = unit / p.split.splits, split = unit % p.split.splits;
-    const int first = tile / (8 * p.tiles_n) * 8, gsz = min(p.tiles_m - first, 8), in = tile % (8 * p.tiles_n);
+    const int first = tile / (4 * p.tiles_n) * 4, gsz = min(p.tiles_m - first, 4), in = tile % (4 * p.tiles_n);
     const int row0 = (first + in % gsz) * BM, col0 = in / gsz * BN;
 
     const int rows = min(p.M - row0, BM), cols = min(p.N - col0, BN);
@@ -364,11 +364,13 @@ void gemm_w4_tiled_kernel(W4Params p) {
 #pragma unroll
         for (int i = 0; i < TI; ++i) acc[i] = sum[i];
     }
+    by_out_type(p.out.d_type, [&](auto type) {
 #pragma unroll
-    for (int i = 0; i < TI; ++i) {
-        const int r = (wm * TI + i) * 32, col = wn * 32 + l32;
-        store_tile(p.out, row0 + r, rows - r, col0 + col, col < cols, acc[i]);
-    }
+        for (int i = 0; i < TI; ++i) {
+            const int r = (wm * TI + i) * 32, col = wn * 32 + l32;
+            store_tile<decltype(type)::value>(p.out, row0 + r, rows - r, col0 + col, col < cols, acc[i]);
+        }
+    });
 }
 
 template <int DT, int QT, int GROUP>

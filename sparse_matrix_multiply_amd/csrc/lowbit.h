@@ -74,6 +74,14 @@ struct Mx8Params {
     int M, K;
 };
 
+// Tiles of the weight gradient (rows: columns of dY; columns: of X) and rows of M per chunk.
+enum WgradTile : int { WGRAD_32x128, WGRAD_64x128, WGRAD_128x128, WGRAD_256x256 };
+inline int wgrad_rows(WgradTile t) {
+    return t == WGRAD_32x128 ? 32 : t == WGRAD_64x128 ? 64 : t == WGRAD_128x128 ? 128 : 256;
+}
+inline int wgrad_cols(WgradTile t) { return t == WGRAD_256x256 ? 256 : 128; }
+constexpr int kWgradChunk = 64;
+
 struct WgradParams {
     const uint8_t *Y;
     int64_t y_pitch;     // bytes
@@ -82,14 +90,11 @@ struct WgradParams {
     const uint32_t *SX;
     int64_t lds;
     int M, N, K;
+    WgradTile tile;
     int tiles_n, tiles_k;
     OutParams out;
     SplitParams split;
 };
-
-// Geometry of the weight-gradient kernel: tile rows for N, tile columns, rows of M per chunk.
-inline int wgrad_rows(int64_t N) { return N <= 32 ? 32 : N <= 64 ? 64 : 128; }
-constexpr int kWgradCols = 128, kWgradChunk = 64;
 
 hipError_t launch_w4_quantize(int w_type, int q_type, bool symmetric, int group, const W4QuantParams &p, hipStream_t s);
 hipError_t launch_gemm_w4_rows(int a_type, int q_type, const W4Params &p, hipStream_t s);
@@ -200,7 +205,7 @@ __device__ __forceinline__ void store_out(const OutParams &o, int64_t i, int64_t
 // 8 (e / 4) + 4 (L / 32) + e mod 4); rows at and past `rows` and lanes with `in` false are left out.  All of C
 // is read before D is written, so that its 16 reads are in flight together (C may be D).
 template <int OT>
-__device__ __forceinline__ void store_tile_as(const OutParams &o, int64_t row0, int rows, int64_t j, bool in, const f32x16 &acc) {
+__device__ __forceinline__ void store_tile(const OutParams &o, int64_t row0, int rows, int64_t j, bool in, const f32x16 &acc) {
     typedef std::conditional_t<OT == OUT_ACC, uint32_t, std::conditional_t<OT <= OUT_F16, uint16_t, uint8_t>> T;
     const int first = (threadIdx.x & 32) / 8;
     const bool has_bias = o.bias != nullptr, relu = o.act != 0;
@@ -224,13 +229,15 @@ __device__ __forceinline__ void store_tile_as(const OutParams &o, int64_t row0, 
         if (r < rows) D[r * o.ldd] = (T)finish<OT>(v, bias, has_bias, relu);
     }
 }
-__device__ __forceinline__ void store_tile(const OutParams &o, int64_t row0, int rows, int64_t j, bool in, const f32x16 &acc) {
-    switch (o.d_type) {
-    case OUT_ACC: return store_tile_as<OUT_ACC>(o, row0, rows, j, in, acc);
-    case OUT_BF16: return store_tile_as<OUT_BF16>(o, row0, rows, j, in, acc);
-    case OUT_F16: return store_tile_as<OUT_F16>(o, row0, rows, j, in, acc);
-    case OUT_E4M3: return store_tile_as<OUT_E4M3>(o, row0, rows, j, in, acc);
-    default: return store_tile_as<OUT_E5M2>(o, row0, rows, j, in, acc);
+// body(integral constant of D's type), so that the choice is made once for all of a wave's tiles.
+template <class F>
+__device__ __forceinline__ void by_out_type(int d_type, F body) {
+    switch (d_type) {
+    case OUT_ACC: return body(std::integral_constant<int, OUT_ACC>{});
+    case OUT_BF16: return body(std::integral_constant<int, OUT_BF16>{});
+    case OUT_F16: return body(std::integral_constant<int, OUT_F16>{});
+    case OUT_E4M3: return body(std::integral_constant<int, OUT_E4M3>{});
+    default: return body(std::integral_constant<int, OUT_E5M2>{});
     }
 }
 

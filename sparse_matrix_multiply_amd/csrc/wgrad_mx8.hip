@@ -56,7 +56,7 @@ __device__ __forceinline__ i32x4 tr_frag(const uint8_t *tile, int n0, int s, int
     return f;
 }
 
-// Sixteen elements of one block -> sixteen DT values (32 bytes), scaled.
+// Sixteen elements of one block -> sixteen DT values (32 bytes), scaled: two elements per instruction for the fp8 types.
 template <int DT, int QT>
 __device__ __forceinline__ void scaled16(const i32x4 &q, uint32_t e, i32x4 (&o)[2]) {
     const float scale = __builtin_bit_cast(float, e == 255 ? 0x7fc00000u : e == 0 ? 0x00400000u : e << 23);
@@ -74,17 +74,21 @@ __device__ __forceinline__ void scaled16(const i32x4 &q, uint32_t e, i32x4 (&o)[
                 lo = __builtin_bit_cast(int, f16x2{(_Float16)f0, (_Float16)f1});
                 hi = __builtin_bit_cast(int, f16x2{(_Float16)f2, (_Float16)f3});
             }
-        } else {
-            // two elements per conversion: fp32 pair, scaled, then rounded to DT
-            const auto a = QT == DT_E4M3 ? __builtin_amdgcn_cvt_pk_f32_fp8(v, false) : __builtin_amdgcn_cvt_pk_f32_bf8(v, false);
-            const auto b = QT == DT_E4M3 ? __builtin_amdgcn_cvt_pk_f32_fp8(v, true) : __builtin_amdgcn_cvt_pk_f32_bf8(v, true);
-            const float f0 = a[0] * scale, f1 = a[1] * scale, f2 = b[0] * scale, f3 = b[1] * scale;
-            if constexpr (DT == DT_BF16) {
-                lo = __builtin_bit_cast(int, bf16x2{(__bf16)f0, (__bf16)f1});
-                hi = __builtin_bit_cast(int, bf16x2{(__bf16)f2, (__bf16)f3});
+        } else if constexpr (DT == DT_BF16) {
+            if constexpr (QT == DT_E4M3) {
+                lo = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v, scale, false));
+                hi = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v, scale, true));
             } else {
-                lo = __builtin_bit_cast(int, f16x2{(_Float16)f0, (_Float16)f1});
-                hi = __builtin_bit_cast(int, f16x2{(_Float16)f2, (_Float16)f3});
+                lo = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(v, scale, false));
+                hi = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(v, scale, true));
+            }
+        } else {
+            if constexpr (QT == DT_E4M3) {
+                lo = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(v, scale, false));
+                hi = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(v, scale, true));
+            } else {
+                lo = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_bf8(v, scale, false));
+                hi = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_bf8(v, scale, true));
             }
         }
         o[d >> 1][2 * (d & 1)] = lo;
@@ -92,21 +96,33 @@ __device__ __forceinline__ void scaled16(const i32x4 &q, uint32_t e, i32x4 (&o)[
     }
 }
 
-template <int DT, int QT, int BN, int WN, int WK>
-__global__ __launch_bounds__(256) void gemm_mx8_wgrad_kernel(WgradParams p) {
-    constexpr int BK = kWgradCols, MC = kWgradChunk, NT = 256;
-    static_assert(WN * WK * 64 == NT, "four waves");
+// BN x BK tile, WN x WK waves, chunks loaded D ahead.
+template <int DT, int QT, int BN, int BK, int WN, int WK, int D>
+__global__ __launch_bounds__(WN * WK * 64) __attribute__((amdgpu_waves_per_eu(2)))
+void gemm_mx8_wgrad_kernel(WgradParams p) {
+    constexpr int MC = kWgradChunk, NT = WN * WK * 64;
     constexpr int TN = BN / WN / 32, TK = BK / WK / 32;
+    constexpr bool SPLIT = BN < 256;                        // the widest tile is only taken where there are tiles enough
     constexpr int UY = BN / 8, UX = BK / 8;                 // 16-byte units per LDS row
     constexpr int YP = MC * UY / NT;                        // copy instructions of dY per chunk
-    constexpr int Y_BYTES = MC * BN * 2, X_BYTES = MC * BK * 2, STAGE = Y_BYTES + X_BYTES;
     constexpr int XU = MC * BK / 16 / NT;                   // 16-element units of X per thread
-    __shared__ __attribute__((aligned(16))) uint8_t smem[2 * STAGE];
+    constexpr int LPT = YP + 2 * XU;                        // memory instructions per chunk
+    constexpr int Y_BYTES = MC * BN * 2, X_BYTES = MC * BK * 2;
+    constexpr int LDS_BYTES = (D + 1) * Y_BYTES + 2 * X_BYTES;
+    static_assert(YP * NT == MC * UY && XU * NT * 16 == MC * BK, "whole copies");
+    static_assert(LDS_BYTES <= 160 * 1024 && (D - 1) * LPT < 64, "LDS and counter range");
+    __shared__ __attribute__((aligned(16))) uint8_t smem[LDS_BYTES];
+    uint8_t *const smem_x = smem + (D + 1) * Y_BYTES;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wn = wave / WK, wk = wave % WK;
-    // ranges of one tile are consecutive workgroups
-    const int split = blockIdx.x % p.split.splits, tile = blockIdx.x / p.split.splits;
-    const int n0 = tile % p.tiles_n * BN, k0 = tile / p.tiles_n * BK;
+    // workgroup -> (tile, range): contiguous runs per XCD, so that the tiles an XCD has at once share their rows of
+    // dY and columns of X in its L2; ranges of one tile are consecutive
+    const int U = p.tiles_n * p.tiles_k * p.split.splits;
+    const int xcd = blockIdx.x & 7, uq = U >> 3, ur = U & 7;
+    const int unit = xcd * uq + (xcd < ur ? xcd : ur) + (blockIdx.x >> 3);
+    const int split = unit % p.split.splits, tile = unit / p.split.splits;
+    const int first = tile / (4 * p.tiles_k) * 4, gsz = min(p.tiles_n - first, 4), in = tile % (4 * p.tiles_k);
+    const int n0 = (first + in % gsz) * BN, k0 = in / gsz * BK;
     const int chunks = (p.M + MC - 1) / MC;
     const int c0 = split * p.split.per_split, c1 = min(c0 + p.split.per_split, chunks);
     const int y_row = (p.N * 2 + 15) / 16 * 16, kp = (p.K + 31) / 32 * 32;
@@ -128,61 +144,86 @@ __global__ __launch_bounds__(256) void gemm_mx8_wgrad_kernel(WgradParams p) {
                                                      (uint32_t)(row * p.y_pitch) + u * 16, 0, 0, 0);
         }
     };
-    i32x4 xq[XU];
-    uint32_t xe[XU];
-    const auto load_x = [&](int c) {
+    i32x4 xq[D][XU];
+    uint32_t xe[D][XU];
+    const auto load_x = [&](int c, int d) {
         const int64_t m0 = (int64_t)c * MC;
         const int rows = (int)min((int64_t)MC, p.M - m0);
         const rsrc_t r = make_rsrc(p.Xq + m0 * p.q_pitch + k0, (uint32_t)((rows - 1) * p.q_pitch + kp - k0));
-        const rsrc_t rs = make_rsrc(p.SX + (k0 / 128) * p.lds + m0, (uint32_t)(rows * 4));
 #pragma unroll
         for (int j = 0; j < XU; ++j) {
             const uint32_t P = j * NT + tid, row = P / (BK / 16), u = P % (BK / 16);
-            xq[j] = __builtin_amdgcn_raw_buffer_load_b128(r, (uint32_t)(row * p.q_pitch) + u * 16, 0, 0);
-            xe[j] = __builtin_amdgcn_raw_buffer_load_b32(rs, row * 4, 0, 0) >> (8 * (u / 2));
+            // a tile of 256 columns has two strips of scale words; the second may lie past the last one
+            const int strip = k0 / 128 + (int)(u / 8);
+            const rsrc_t rs = make_rsrc(p.SX + (k0 / 128) * p.lds + m0, (uint32_t)(((p.K + 127) / 128 - k0 / 128 - 1) * p.lds * 4 + rows * 4));
+            xq[d][j] = __builtin_amdgcn_raw_buffer_load_b128(r, (uint32_t)(row * p.q_pitch) + u * 16, 0, 0);
+            xe[d][j] = __builtin_amdgcn_raw_buffer_load_b32(
+                rs, (int)row < rows ? (uint32_t)(((strip - k0 / 128) * p.lds + row) * 4) : kOutOfRange, 0, 0);
         }
     };
-    const auto put_x = [&](uint8_t *st) {
+    // the two halves of a unit in an order in which 16 lanes' writes meet 16 bank groups
+    const auto put_x = [&](uint8_t *st, int d) {
 #pragma unroll
         for (int j = 0; j < XU; ++j) {
             const uint32_t P = j * NT + tid, row = P / (BK / 16), u = P % (BK / 16);
             i32x4 o[2];
-            scaled16<DT, QT>(xq[j], xe[j] & 255u, o);
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-                *reinterpret_cast<i32x4 *>(st + Y_BYTES + row * (BK * 2) + (((2 * u + h) ^ tr_swz<UX>(row)) << 4)) = o[h];
+            scaled16<DT, QT>(xq[d][j], (xe[d][j] >> (8 * ((u / 2) & 3))) & 255u, o);
+            const bool swap = lane & 8;
+            const i32x4 w0 = swap ? o[1] : o[0], w1 = swap ? o[0] : o[1];
+            uint8_t *at = st + row * (BK * 2);
+            *reinterpret_cast<i32x4 *>(at + (((2 * u + (swap ? 1 : 0)) ^ tr_swz<UX>(row)) << 4)) = w0;
+            *reinterpret_cast<i32x4 *>(at + (((2 * u + (swap ? 0 : 1)) ^ tr_swz<UX>(row)) << 4)) = w1;
         }
     };
 
-    if (c0 < c1) {
-        copy_y(c0, smem);
-        load_x(c0);
-    }
-    for (int c = c0; c < c1; ++c) {
-        uint8_t *st = smem + ((c - c0) & 1) * STAGE;
-        put_x(st);             // its last readers passed the barrier before this one
-        wait_vm_lgkm0<0>();
-        block_barrier();
-        if (c + 1 < c1) {
-            copy_y(c + 1, smem + ((c + 1 - c0) & 1) * STAGE);
-            load_x(c + 1);
+#pragma unroll
+    for (int d = 0; d < D; ++d)
+        if (c0 + d < c1) {
+            copy_y(c0 + d, smem + d * Y_BYTES);
+            load_x(c0 + d, d);
         }
+    int ys = 0;   // dY's stage of chunk c
+    const auto chunk = [&](int c, int d) {
+        uint8_t *sx = smem_x + ((c - c0) & 1) * X_BYTES;
+        const uint8_t *sy = smem + ys * Y_BYTES;
+        // dY's copy of chunk c has landed when at most the D - 1 chunks issued after it are outstanding
+        if (c + D <= c1) wait_vm_lgkm0<(D - 1) * LPT>();
+        else wait_vm_lgkm0<0>();
+        put_x(sx, d);          // its last readers passed the barrier before this one
+        wait_lds();
+        block_barrier();
+        if (c + D < c1) {
+            copy_y(c + D, smem + (ys == 0 ? D : ys - 1) * Y_BYTES);
+            load_x(c + D, d);
+        }
+        i32x4 a[2][TN], b[2][TK];
+        const auto read = [&](int s) {
+#pragma unroll
+            for (int i = 0; i < TN; ++i) a[s & 1][i] = tr_frag<BN>(sy, (wn * TN + i) * 32, s, lane);
+#pragma unroll
+            for (int j = 0; j < TK; ++j) b[s & 1][j] = tr_frag<BK>(sx, (wk * TK + j) * 32, s, lane);
+        };
+        read(0);
 #pragma unroll
         for (int s = 0; s < MC / 16; ++s) {
-            i32x4 a[TN], b[TK];
-#pragma unroll
-            for (int i = 0; i < TN; ++i) a[i] = tr_frag<BN>(st, (wn * TN + i) * 32, s, lane);
-#pragma unroll
-            for (int j = 0; j < TK; ++j) b[j] = tr_frag<BK>(st + Y_BYTES, (wk * TK + j) * 32, s, lane);
+            __builtin_amdgcn_sched_barrier(0);   // keeps a step's reads a step ahead of their use
+            if (s + 1 < MC / 16) read(s + 1);
 #pragma unroll
             for (int i = 0; i < TN; ++i)
 #pragma unroll
-                for (int j = 0; j < TK; ++j) acc[i][j] = mma32<DT>(a[i], b[j], acc[i][j]);
+                for (int j = 0; j < TK; ++j) acc[i][j] = mma32<DT>(a[s & 1][i], b[s & 1][j], acc[i][j]);
         }
+        __builtin_amdgcn_sched_barrier(0);
+        ys = ys == D ? 0 : ys + 1;
+    };
+    for (int c = c0; c < c1; c += D) {
+#pragma unroll
+        for (int d = 0; d < D; ++d)
+            if (c + d < c1) chunk(c + d, d);
     }
 
     // ranges joined by the last to arrive, in range order (the partials at device scope, see the tiled GEMM)
-    if (p.split.splits > 1) {
+    if (SPLIT && p.split.splits > 1) {
         constexpr int TILE_BYTES = BN * BK * 4;
         uint8_t *ws = p.split.partials + (int64_t)tile * p.split.splits * TILE_BYTES;
         const rsrc_t mine = make_rsrc(ws + (int64_t)split * TILE_BYTES, TILE_BYTES);
@@ -208,43 +249,60 @@ __global__ __launch_bounds__(256) void gemm_mx8_wgrad_kernel(WgradParams p) {
         }
         __syncthreads();
         if (*arrived != (uint32_t)p.split.splits - 1) return;
+        constexpr int BATCH = TN * TK == 1 ? 4 : TN * TK == 2 ? 2 : 1;   // ranges whose loads are in flight together
+        f32x16 sum[TN][TK];
+        for (int r0 = 0; r0 < p.split.splits; r0 += BATCH) {
+            i32x4 v[BATCH][TN][TK][4];
+#pragma unroll
+            for (int b = 0; b < BATCH; ++b) {
+                const bool real = r0 + b < p.split.splits;   // past the last range: offsets past the buffer, zeros
+                const rsrc_t part = make_rsrc(ws + (int64_t)(real ? r0 + b : 0) * TILE_BYTES, TILE_BYTES);
+#pragma unroll
+                for (int i = 0; i < TN; ++i)
+#pragma unroll
+                    for (int j = 0; j < TK; ++j)
+#pragma unroll
+                        for (int g = 0; g < 4; ++g)
+                            v[b][i][j][g] = __builtin_amdgcn_raw_buffer_load_b128(
+                                part, real ? (uint32_t)((((i * TK + j) * 4 + g) * NT + tid) * 16) : kOutOfRange, 0, kDeviceScope);
+            }
+#pragma unroll
+            for (int b = 0; b < BATCH; ++b)
+#pragma unroll
+                for (int i = 0; i < TN; ++i)
+#pragma unroll
+                    for (int j = 0; j < TK; ++j)
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            const int w = v[b][i][j][e / 4][e % 4];
+                            const float f = __builtin_bit_cast(float, w);
+                            sum[i][j][e] = r0 == 0 && b == 0 ? f : sum[i][j][e] + f;
+                        }
+        }
+#pragma unroll
+        for (int i = 0; i < TN; ++i)
+#pragma unroll
+            for (int j = 0; j < TK; ++j) acc[i][j] = sum[i][j];
+    }
+    by_out_type(p.out.d_type, [&](auto type) {
 #pragma unroll
         for (int i = 0; i < TN; ++i)
 #pragma unroll
             for (int j = 0; j < TK; ++j) {
-                f32x16 sum = {};
-                for (int r = 0; r < p.split.splits; ++r) {
-                    const rsrc_t part = make_rsrc(ws + (int64_t)r * TILE_BYTES, TILE_BYTES);
-#pragma unroll
-                    for (int g = 0; g < 4; ++g) {
-                        const i32x4 v = __builtin_amdgcn_raw_buffer_load_b128(
-                            part, (uint32_t)((((i * TK + j) * 4 + g) * NT + tid) * 16), 0, kDeviceScope);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const int w = v[e];
-                            sum[4 * g + e] += __builtin_bit_cast(float, w);
-                        }
-                    }
-                }
-                acc[i][j] = sum;
+                const int n = n0 + (wn * TN + i) * 32, k = k0 + (wk * TK + j) * 32 + (lane & 31);
+                store_tile<decltype(type)::value>(p.out, n, p.N - n, k, k < p.K, acc[i][j]);
             }
-    }
-#pragma unroll
-    for (int i = 0; i < TN; ++i)
-#pragma unroll
-        for (int j = 0; j < TK; ++j) {
-            const int n = n0 + (wn * TN + i) * 32, k = k0 + (wk * TK + j) * 32 + (lane & 31);
-            store_tile(p.out, n, p.N - n, k, k < p.K, acc[i][j]);
-        }
+    });
 }
 
 template <int DT, int QT>
 static hipError_t launch_as(const WgradParams &p, hipStream_t s) {
-    const dim3 grid((unsigned)(p.tiles_n * p.tiles_k * p.split.splits)), block(256);
-    switch (wgrad_rows(p.N)) {
-    case 32: hipLaunchKernelGGL((gemm_mx8_wgrad_kernel<DT, QT, 32, 1, 4>), grid, block, 0, s, p); break;
-    case 64: hipLaunchKernelGGL((gemm_mx8_wgrad_kernel<DT, QT, 64, 1, 4>), grid, block, 0, s, p); break;
-    default: hipLaunchKernelGGL((gemm_mx8_wgrad_kernel<DT, QT, 128, 2, 2>), grid, block, 0, s, p); break;
+    const dim3 grid((unsigned)(p.tiles_n * p.tiles_k * p.split.splits));
+    switch (p.tile) {
+    case WGRAD_32x128: hipLaunchKernelGGL((gemm_mx8_wgrad_kernel<DT, QT, 32, 128, 1, 4, 4>), grid, dim3(256), 0, s, p); break;
+    case WGRAD_64x128: hipLaunchKernelGGL((gemm_mx8_wgrad_kernel<DT, QT, 64, 128, 1, 4, 3>), grid, dim3(256), 0, s, p); break;
+    case WGRAD_128x128: hipLaunchKernelGGL((gemm_mx8_wgrad_kernel<DT, QT, 128, 128, 2, 2, 2>), grid, dim3(256), 0, s, p); break;
+    default: hipLaunchKernelGGL((gemm_mx8_wgrad_kernel<DT, QT, 256, 256, 2, 4, 2>), grid, dim3(512), 0, s, p); break;
     }
     return hipGetLastError();
 }
