@@ -364,13 +364,13 @@ void gemm_w4_tiled_kernel(W4Params p) {
 #pragma unroll
         for (int i = 0; i < TI; ++i) acc[i] = sum[i];
     }
-    by_out_type(p.out.d_type, [&](auto type) {
 #pragma unroll
-        for (int i = 0; i < TI; ++i) {
-            const int r = (wm * TI + i) * 32, col = wn * 32 + l32;
+    for (int i = 0; i < TI; ++i) {
+        const int r = (wm * TI + i) * 32, col = wn * 32 + l32;
+        by_out_type(p.out.d_type, [&](auto type) {
             store_tile<decltype(type)::value>(p.out, row0 + r, rows - r, col0 + col, col < cols, acc[i]);
-        }
-    });
+        });
+    }
 }
 
 template <int DT, int QT, int GROUP>

@@ -9,18 +9,19 @@
 //
 // Both kernels stream, so HBM sets their time.  A lane holds eight elements of
 // a row (16 bytes of a 16-bit type), four lanes a block, sixteen lanes the 128
-// columns of one scale word; a wave covers 128 columns of 4 rows per step and
-// 32 rows in all.  Scale words are stored column-major (one 128-column strip
-// after the other), so a wave's 32 words of one strip are one 128-byte line:
-// the quantizer gathers them in LDS and writes them with one store.
+// columns of one scale word; an instruction of a wave covers 512 columns of one
+// row (1 KiB of a 16-bit type), a wave 8 rows with all their loads in flight.
+// Scale words are stored column-major (one 128-column strip after the other), so
+// the workgroup's 32 words of one strip are one 128-byte line: the quantizer
+// gathers them in LDS and writes whole lines.
 #include <algorithm>
 
 #include "lowbit.h"
 
 namespace mmac {
 
-constexpr int kRows = 32;           // rows of a wave
-constexpr int kSteps = kRows / 4;   // 4 rows per step
+// A workgroup's unit: 512 columns of 32 rows, 8 rows a wave.
+constexpr int kRows = 32, kSteps = kRows / 4, kCols = 512;
 
 template <int QT> struct Mx8Type;
 template <> struct Mx8Type<DT_E4M3> { static constexpr int top = 8; static constexpr uint32_t frac = 0x600000; };
@@ -66,23 +67,23 @@ __device__ __forceinline__ u32x2 to_elements(const float (&y)[8], bool odd) {
 }
 
 template <int XT, int QT>
-__global__ __launch_bounds__(256) void mx8_quantize_kernel(Mx8Params p, int64_t units, int strips) {
-    __shared__ uint32_t words[4][kRows];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l16 = lane & 15, quarter = lane >> 4;
-    const int kp = (p.K + 31) / 32 * 32;
-    for (int64_t unit = (int64_t)blockIdx.x * 4 + wave; unit < units; unit += (int64_t)gridDim.x * 4) {
-        const int strip = (int)(unit % strips);
-        const int64_t row0 = unit / strips * kRows;
-        const int e0 = strip * 128 + l16 * 8;
+__global__ __launch_bounds__(256) void mx8_quantize_kernel(Mx8Params p, int64_t units, int blocks) {
+    __shared__ uint32_t words[kCols / 128][kRows];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l16 = lane & 15;
+    const int kp = (p.K + 31) / 32 * 32, strips = (p.K + 127) / 128;
+    for (int64_t unit = blockIdx.x; unit < units; unit += gridDim.x) {
+        const int block = (int)(unit % blocks);
+        const int64_t row0 = unit / blocks * kRows;
+        const int e0 = block * kCols + lane * 8;
         float x[kSteps][8];
 #pragma unroll
         for (int s = 0; s < kSteps; ++s) {
-            const int64_t row = row0 + 4 * s + quarter;
+            const int64_t row = row0 + wave * kSteps + s;
             load8<XT>(x[s], p.X + row * p.x_pitch, e0, row < p.M ? p.K : 0);
         }
 #pragma unroll
         for (int s = 0; s < kSteps; ++s) {
-            const int64_t row = row0 + 4 * s + quarter;
+            const int64_t row = row0 + wave * kSteps + s;
             // largest magnitude (fp32 bits order like magnitudes) over the finite elements, and whether all are
             uint32_t m = 0, worst = 0;
 #pragma unroll
@@ -114,36 +115,40 @@ __global__ __launch_bounds__(256) void mx8_quantize_kernel(Mx8Params p, int64_t 
             uint32_t w = (uint32_t)e << (8 * (l16 >> 2));
             w |= dpp<kDppRor4>(w);
             w |= dpp<kDppRor8>(w);
-            if (l16 == 0) words[wave][4 * s + quarter] = w;
+            if (l16 == 0) words[lane >> 4][wave * kSteps + s] = w;
         }
-        wave_sync();
-        const int64_t row = row0 + lane;
-        if (lane < kRows && row < p.M) const_cast<uint32_t *>(p.SX)[strip * p.lds + row] = words[wave][lane];
-        wave_sync();
+        __syncthreads();
+        if (threadIdx.x < kCols / 128 * kRows) {
+            const int strip = block * (kCols / 128) + threadIdx.x / kRows;
+            const int64_t row = row0 + threadIdx.x % kRows;
+            if (strip < strips && row < p.M)
+                const_cast<uint32_t *>(p.SX)[strip * p.lds + row] = words[threadIdx.x / kRows][threadIdx.x % kRows];
+        }
+        __syncthreads();   // before the next unit's words
     }
 }
 
 template <int QT, int XT>
-__global__ __launch_bounds__(256) void mx8_dequantize_kernel(Mx8Params p, int64_t units, int strips) {
+__global__ __launch_bounds__(256) void mx8_dequantize_kernel(Mx8Params p, int64_t units, int blocks) {
     constexpr int ES = dt_size<XT>();
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l16 = lane & 15, quarter = lane >> 4;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l16 = lane & 15;
     const int kp = (p.K + 31) / 32 * 32;
-    for (int64_t unit = (int64_t)blockIdx.x * 4 + wave; unit < units; unit += (int64_t)gridDim.x * 4) {
-        const int strip = (int)(unit % strips);
-        const int64_t row0 = unit / strips * kRows;
-        const int e0 = strip * 128 + l16 * 8;
+    for (int64_t unit = blockIdx.x; unit < units; unit += gridDim.x) {
+        const int block = (int)(unit % blocks), strip = block * (kCols / 128) + (lane >> 4);
+        const int64_t row0 = unit / blocks * kRows;
+        const int e0 = block * kCols + lane * 8;
         u32x2 q[kSteps];
         uint32_t w[kSteps];
 #pragma unroll
         for (int s = 0; s < kSteps; ++s) {
-            const int64_t row = row0 + 4 * s + quarter;
+            const int64_t row = row0 + wave * kSteps + s;
             const bool in = row < p.M && e0 < kp;
             q[s] = in ? *reinterpret_cast<const u32x2 *>(p.Xq + row * p.q_pitch + e0) : u32x2{0, 0};
             w[s] = in ? p.SX[strip * p.lds + row] : 0;
         }
 #pragma unroll
         for (int s = 0; s < kSteps; ++s) {
-            const int64_t row = row0 + 4 * s + quarter;
+            const int64_t row = row0 + wave * kSteps + s;
             const uint32_t e = (w[s] >> (8 * (l16 >> 2))) & 255u;
             const float scale = __builtin_bit_cast(float, e == 255 ? 0x7fc00000u : e == 0 ? 0x00400000u : e << 23);
             float v[8];
@@ -196,23 +201,21 @@ __global__ __launch_bounds__(256) void mx8_dequantize_kernel(Mx8Params p, int64_
     }
 }
 
-// Waves' units (strips of 128 columns x 32 rows) over a grid that the device limits; what it does not hold at
-// once the waves walk over.
-static dim3 grid_of(int64_t units) { return dim3((unsigned)std::min<int64_t>((units + 3) / 4, 1 << 20)); }
-
-template <int XT, int QT>
-static hipError_t quantize_as(const Mx8Params &p, hipStream_t s) {
-    const int strips = (p.K + 127) / 128;
-    const int64_t units = (int64_t)strips * ((p.M + kRows - 1) / kRows);
-    hipLaunchKernelGGL((mx8_quantize_kernel<XT, QT>), grid_of(units), dim3(256), 0, s, p, units, strips);
+// Workgroups over units; what the grid does not hold at once they walk over.
+template <class K>
+static hipError_t launch_units(K kernel, const Mx8Params &p, hipStream_t s) {
+    const int blocks = (p.K + kCols - 1) / kCols;
+    const int64_t units = (int64_t)blocks * ((p.M + kRows - 1) / kRows);
+    hipLaunchKernelGGL(kernel, dim3((unsigned)std::min<int64_t>(units, 1 << 20)), dim3(256), 0, s, p, units, blocks);
     return hipGetLastError();
 }
 template <int XT, int QT>
+static hipError_t quantize_as(const Mx8Params &p, hipStream_t s) {
+    return launch_units(mx8_quantize_kernel<XT, QT>, p, s);
+}
+template <int XT, int QT>
 static hipError_t dequantize_as(const Mx8Params &p, hipStream_t s) {
-    const int strips = (p.K + 127) / 128;
-    const int64_t units = (int64_t)strips * ((p.M + kRows - 1) / kRows);
-    hipLaunchKernelGGL((mx8_dequantize_kernel<QT, XT>), grid_of(units), dim3(256), 0, s, p, units, strips);
-    return hipGetLastError();
+    return launch_units(mx8_dequantize_kernel<QT, XT>, p, s);
 }
 
 template <int XT>

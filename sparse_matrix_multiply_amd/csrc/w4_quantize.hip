@@ -9,9 +9,11 @@
 //
 // The work is a streaming pass, bound by HBM.  Groups of 32 to 128: a lane
 // holds eight elements, 4 to 16 lanes a group, a wave 128 columns of 32 rows; the
-// scale words (group-major) are gathered in LDS so that a wave writes 32
-// consecutive ones at a time.  Whole rows: one workgroup per row reads the row
-// twice, the second time from the caches.
+// scale words (group-major) are gathered in LDS so that 32 consecutive ones are
+// written at a time.  Whole rows: one workgroup per row reads the row twice, the
+// second time from the caches.  A division per element would take longer than the
+// memory does; the product with 1 / s (off by less than 4e-6 for quotients up
+// to 15) decides everywhere but within 1e-5 of a middle.
 #include <algorithm>
 
 #include "lowbit.h"
@@ -79,49 +81,67 @@ __device__ __forceinline__ uint32_t scale_word(const Range &r, float &s, float &
     return u | (uint32_t)z;
 }
 
+// Code of x for scale s > 0; inv = 1 / s rounded.
 template <int QT>
-__device__ __forceinline__ uint32_t code_of(float x, float s, float z) {
+__device__ __forceinline__ uint32_t code_of(float x, float s, float inv, float z) {
+    constexpr float kNear = 1e-5f;
+    const float q = x * inv;
     if constexpr (QT == DT_FP4) {
-        if (s == 0.0f) return 0;
-        return nearest_e2m1(__builtin_fabsf(x), s) | (x < 0.0f ? 8u : 0u);
+        // steps of 1/2 below 2, of 1 below 4, of 2 above: in units of the step the code is the nearest integer plus 0, 2, 4
+        const float a = __builtin_fabsf(q);
+        const float per = a < 2.0f ? 2.0f : a < 4.0f ? 1.0f : 0.5f, base = a < 2.0f ? 0.0f : a < 4.0f ? 2.0f : 4.0f;
+        const float y = a * per, n = __builtin_rintf(y);
+        uint32_t code = (uint32_t)fminf(n + base, 7.0f);
+        if (__builtin_fabsf(__builtin_fabsf(y - n) - 0.5f) < kNear) code = nearest_e2m1(__builtin_fabsf(x), s);
+        return code | (x < 0.0f ? 8u : 0u);
     } else {
-        if (s == 0.0f) return (uint32_t)z;
-        return (uint32_t)fminf(fmaxf(nearest_quotient(x, s) + z, 0.0f), 15.0f);
+        float n = __builtin_rintf(q);
+        if (__builtin_fabsf(__builtin_fabsf(q - n) - 0.5f) < kNear) n = nearest_quotient(x, s);
+        return (uint32_t)fminf(fmaxf(n + z, 0.0f), 15.0f);
     }
 }
 
 // Eight codes of a lane's elements e0 .. e0 + 7, those at and past K zero.
 template <int QT>
 __device__ __forceinline__ uint32_t codes_of(const float (&x)[8], float s, float z, int e0, int K) {
+    if (s == 0.0f) {   // every code is z
+        uint32_t w = (uint32_t)z * 0x11111111u;
+        if (e0 + 8 > K) w = e0 >= K ? 0u : w & ((1u << (4 * (K - e0))) - 1u);
+        return w;
+    }
+    const float inv = 1.0f / s;
     uint32_t w = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        if (e0 + i < K) w |= code_of<QT>(x[i], s, z) << (4 * i);
+    for (int i = 0; i < 8; ++i) {
+        const uint32_t c = code_of<QT>(x[i], s, inv, z);
+        if (e0 + i < K) w |= c << (4 * i);
+    }
     return w;
 }
 
-constexpr int kRows = 32, kSteps = kRows / 4;
+// A workgroup's unit: 512 columns of 32 rows, 8 rows a wave; an instruction of a wave covers 512 columns of one row.
+constexpr int kRows = 32, kSteps = kRows / 4, kCols = 512;
 
 template <int WT, int QT, bool SYM, int GROUP>
-__global__ __launch_bounds__(256) void w4_quantize_kernel(W4QuantParams p, int64_t units, int strips) {
-    constexpr int LANES = GROUP / 8, PER = 128 / GROUP;   // lanes of a group, groups of a strip
-    __shared__ uint32_t words[4][PER][kRows];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l16 = lane & 15, quarter = lane >> 4;
+__global__ __launch_bounds__(256) void w4_quantize_kernel(W4QuantParams p, int64_t units, int blocks) {
+    constexpr int LANES = GROUP / 8, PER = kCols / GROUP;   // lanes of a group, groups of a unit's row
+    __shared__ uint32_t words[PER][kRows];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int kp = (p.K + 31) / 32 * 32;
     const int groups = (p.K + GROUP - 1) / GROUP;
-    for (int64_t unit = (int64_t)blockIdx.x * 4 + wave; unit < units; unit += (int64_t)gridDim.x * 4) {
-        const int strip = (int)(unit % strips);
-        const int64_t row0 = unit / strips * kRows;
-        const int e0 = strip * 128 + l16 * 8;
+    for (int64_t unit = blockIdx.x; unit < units; unit += gridDim.x) {
+        const int block = (int)(unit % blocks);
+        const int64_t row0 = unit / blocks * kRows;
+        const int e0 = block * kCols + lane * 8;
         float x[kSteps][8];
 #pragma unroll
         for (int st = 0; st < kSteps; ++st) {
-            const int64_t row = row0 + 4 * st + quarter;
+            const int64_t row = row0 + wave * kSteps + st;
             load8<WT>(x[st], p.W + row * p.w_pitch, e0, row < p.N ? p.K : 0);
         }
 #pragma unroll
         for (int st = 0; st < kSteps; ++st) {
-            const int64_t row = row0 + 4 * st + quarter;
+            const int64_t row = row0 + wave * kSteps + st;
             Range r;
 #pragma unroll
             for (int i = 0; i < 8; ++i) r.add(x[st][i]);
@@ -140,16 +160,15 @@ __global__ __launch_bounds__(256) void w4_quantize_kernel(W4QuantParams p, int64
             const uint32_t word = scale_word<QT, SYM>(r, s, z);
             const uint32_t q = codes_of<QT>(x[st], s, z, e0, p.K);
             if (row < p.N && e0 < kp) *reinterpret_cast<uint32_t *>(p.codes + row * p.pitch + e0 / 2) = q;
-            if (l16 % LANES == 0) words[wave][l16 / LANES][4 * st + quarter] = word;
+            if (lane % LANES == 0) words[lane / LANES][wave * kSteps + st] = word;
         }
-        wave_sync();
-#pragma unroll
-        for (int j = 0; j < (PER + 1) / 2; ++j) {
-            const int g = 2 * j + lane / kRows, group = strip * PER + g;
-            const int64_t row = row0 + lane % kRows;
-            if (g < PER && group < groups && row < p.N) p.words[group * p.ldw + row] = words[wave][g][lane % kRows];
+        __syncthreads();
+        for (int i = threadIdx.x; i < PER * kRows; i += 256) {
+            const int group = block * PER + i / kRows;
+            const int64_t row = row0 + i % kRows;
+            if (group < groups && row < p.N) p.words[group * p.ldw + row] = words[i / kRows][i % kRows];
         }
-        wave_sync();
+        __syncthreads();   // before the next unit's words
     }
 }
 
@@ -202,13 +221,13 @@ static hipError_t launch_as(int group, const W4QuantParams &p, hipStream_t s) {
         hipLaunchKernelGGL((w4_quantize_rows_kernel<WT, QT, SYM>), dim3((unsigned)std::min(p.N, 1 << 20)), dim3(256), 0, s, p);
         return hipGetLastError();
     }
-    const int strips = (p.K + 127) / 128;
-    const int64_t units = (int64_t)strips * ((p.N + kRows - 1) / kRows);
-    const dim3 grid((unsigned)std::min<int64_t>((units + 3) / 4, 1 << 20)), block(256);
+    const int blocks = (p.K + kCols - 1) / kCols;
+    const int64_t units = (int64_t)blocks * ((p.N + kRows - 1) / kRows);
+    const dim3 grid((unsigned)std::min<int64_t>(units, 1 << 20)), block(256);
     switch (group) {
-    case 32: hipLaunchKernelGGL((w4_quantize_kernel<WT, QT, SYM, 32>), grid, block, 0, s, p, units, strips); break;
-    case 64: hipLaunchKernelGGL((w4_quantize_kernel<WT, QT, SYM, 64>), grid, block, 0, s, p, units, strips); break;
-    case 128: hipLaunchKernelGGL((w4_quantize_kernel<WT, QT, SYM, 128>), grid, block, 0, s, p, units, strips); break;
+    case 32: hipLaunchKernelGGL((w4_quantize_kernel<WT, QT, SYM, 32>), grid, block, 0, s, p, units, blocks); break;
+    case 64: hipLaunchKernelGGL((w4_quantize_kernel<WT, QT, SYM, 64>), grid, block, 0, s, p, units, blocks); break;
+    case 128: hipLaunchKernelGGL((w4_quantize_kernel<WT, QT, SYM, 128>), grid, block, 0, s, p, units, blocks); break;
     default: return hipErrorInvalidValue;
     }
     return hipGetLastError();
