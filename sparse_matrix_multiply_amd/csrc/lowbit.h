@@ -111,14 +111,16 @@ typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 template <int DT> constexpr int dt_size() { return DT == DT_F32 ? 4 : DT == DT_F16 || DT == DT_BF16 ? 2 : 1; }
 
 // Eight consecutive elements of a row of type DT, from element e0, as fp32; those at and past `limit` zero.
-template <int DT>
+// STREAM: read past the caches' retention (data that no one reads again; 8192^2 bf16 quantized 5 % faster).
+template <int DT, bool STREAM = false>
 __device__ __forceinline__ void load8(float (&x)[8], const uint8_t *row, int64_t e0, int64_t limit) {
     constexpr int ES = dt_size<DT>();
     if (e0 + 8 <= limit) {
         uint32_t w[2 * ES];
 #pragma unroll
         for (int v = 0; v < ES / 2; ++v) {
-            const i32x4 d = reinterpret_cast<const i32x4 *>(row + e0 * ES)[v];
+            const i32x4 *at = reinterpret_cast<const i32x4 *>(row + e0 * ES) + v;
+            const i32x4 d = STREAM ? __builtin_nontemporal_load(at) : *at;
 #pragma unroll
             for (int i = 0; i < 4; ++i) w[4 * v + i] = (uint32_t)d[i];
         }

@@ -79,7 +79,7 @@ __global__ __launch_bounds__(256) void mx8_quantize_kernel(Mx8Params p, int64_t 
 #pragma unroll
         for (int s = 0; s < kSteps; ++s) {
             const int64_t row = row0 + wave * kSteps + s;
-            load8<XT>(x[s], p.X + row * p.x_pitch, e0, row < p.M ? p.K : 0);
+            load8<XT, true>(x[s], p.X + row * p.x_pitch, e0, row < p.M ? p.K : 0);
         }
 #pragma unroll
         for (int s = 0; s < kSteps; ++s) {

@@ -20,6 +20,15 @@
 
 namespace mmac {
 
+// r / N correctly rounded: the product with the rounded reciprocal, corrected once by the remainder (checked
+// for every significand with N = 6, 7 and 15).
+template <int N>
+__device__ __forceinline__ float divide_by(float r) {
+    constexpr float inv = 1.0f / N;
+    const float q = r * inv;
+    return fmaf(fmaf(-(float)N, q, r), inv, q);
+}
+
 // The integer nearest to a / s (s > 0), ties to even, exact quotient.
 __device__ __forceinline__ float nearest_quotient(float a, float s) {
     const float q = a / s, n = __builtin_rintf(q);
@@ -48,26 +57,53 @@ __device__ __forceinline__ uint32_t nearest_e2m1(float a, float s) {
     return code;
 }
 
-// Range of a group's values, gathered over elements and lanes.
+// Range of a group's values as fp32 bits, which order non-negative values as integers do.  Not symmetric: the
+// largest value and the largest of the negated ones, both at least 0; else the largest magnitude.  A value that is
+// not finite makes the largest one NaN or infinite.
+template <bool SYM>
 struct Range {
-    float lo = 0.0f, hi = 0.0f;
-    uint32_t top = 0;   // bits of the largest magnitude; non-finite values are the largest
-    __device__ __forceinline__ void add(float x) {
-        lo = fminf(lo, x);
-        hi = fmaxf(hi, x);
-        top = max(top, __builtin_bit_cast(uint32_t, x) & 0x7fffffffu);
+    uint32_t hi = 0, neg = 0;
+    __device__ __forceinline__ void add(const float (&x)[8]) {
+        if constexpr (SYM) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) hi = max(hi, __builtin_bit_cast(uint32_t, x[i]) & 0x7fffffffu);
+        } else {
+            float h = __builtin_bit_cast(float, hi), l = -__builtin_bit_cast(float, neg), finite = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                h = fmaxf(h, x[i]);
+                l = fminf(l, x[i]);
+                finite = fmaf(x[i], 0.0f, finite);   // NaN from a NaN or an infinity
+            }
+            hi = finite == 0.0f ? __builtin_bit_cast(uint32_t, h) : 0x7fc00000u;
+            neg = __builtin_bit_cast(uint32_t, -l) & 0x7fffffffu;
+        }
+    }
+    // over groups of LANES consecutive lanes, in every lane
+    template <int LANES>
+    __device__ __forceinline__ void gather() {
+        const auto larger = [](uint32_t a, uint32_t b) { return max(a, b); };
+        hi = reduce_lanes<LANES>(hi, larger);
+        if constexpr (!SYM) neg = reduce_lanes<LANES>(neg, larger);
+    }
+    __device__ __forceinline__ float width() const {
+        const float h = __builtin_bit_cast(float, hi);
+        return SYM ? h : h + __builtin_bit_cast(float, neg);
     }
 };
 
-// The scale word's scale and zero point.
+// How near to a middle between two codes a quotient formed with 1 / s may be believed.
+constexpr float kNear = 1e-5f;
+
+// The scale word, its scale and zero point, and about 1 / s.
 template <int QT, bool SYM>
-__device__ __forceinline__ uint32_t scale_word(const Range &r, float &s, float &z) {
-    const float top = __builtin_bit_cast(float, r.top);
-    const float steps = QT == DT_FP4 ? 6.0f : SYM ? 7.0f : 15.0f;
-    s = (QT == DT_FP4 || SYM ? top : r.hi - r.lo) / steps;
+__device__ __forceinline__ uint32_t scale_word(const Range<SYM> &r, float &s, float &inv, float &z) {
+    static_assert(SYM || QT != DT_FP4, "E2M1 codes have no zero point");
+    s = divide_by<QT == DT_FP4 ? 6 : SYM ? 7 : 15>(r.width());
+    inv = 0.0f;
     z = QT == DT_FP4 ? 0.0f : SYM ? 8.0f : 0.0f;
     uint32_t u = __builtin_bit_cast(uint32_t, s);
-    if (r.top >= 0x7f800000u || u >= 0x7f800000u) {      // a NaN, an infinity, or a range past fp32
+    if (u >= 0x7f800000u) {      // a NaN, an infinity, or a range past fp32
         s = 0.0f;
         return 0x7fc00000u | (uint32_t)z;
     }
@@ -77,45 +113,63 @@ __device__ __forceinline__ uint32_t scale_word(const Range &r, float &s, float &
     }
     u = (u + 0x7fu + ((u >> 8) & 1u)) & ~0xffu;
     s = __builtin_bit_cast(float, u);
-    if (QT != DT_FP4 && !SYM) z = fminf(fmaxf(nearest_quotient(-r.lo, s), 0.0f), 15.0f);
+    inv = __builtin_amdgcn_rcpf(s);   // off by at most one unit of its last place
+    if (QT != DT_FP4 && !SYM) {
+        const float neg = __builtin_bit_cast(float, r.neg), q = neg * inv;
+        float n = __builtin_rintf(q);
+        if (__builtin_fabsf(q - n) > 0.5f - kNear) n = nearest_quotient(neg, s);
+        z = fminf(fmaxf(n, 0.0f), 15.0f);
+    }
     return u | (uint32_t)z;
 }
 
-// Code of x for scale s > 0; inv = 1 / s rounded.
+// Code of x for scale s > 0, inv about 1 / s, before its sign, as a float; `off`: largest distance from a code.
 template <int QT>
-__device__ __forceinline__ uint32_t code_of(float x, float s, float inv, float z) {
-    constexpr float kNear = 1e-5f;
-    const float q = x * inv;
+__device__ __forceinline__ float code_of(float x, float inv, float z, float &off) {
     if constexpr (QT == DT_FP4) {
         // steps of 1/2 below 2, of 1 below 4, of 2 above: in units of the step the code is the nearest integer plus 0, 2, 4
-        const float a = __builtin_fabsf(q);
+        const float a = __builtin_fabsf(x * inv);
         const float per = a < 2.0f ? 2.0f : a < 4.0f ? 1.0f : 0.5f, base = a < 2.0f ? 0.0f : a < 4.0f ? 2.0f : 4.0f;
         const float y = a * per, n = __builtin_rintf(y);
-        uint32_t code = (uint32_t)fminf(n + base, 7.0f);
-        if (__builtin_fabsf(__builtin_fabsf(y - n) - 0.5f) < kNear) code = nearest_e2m1(__builtin_fabsf(x), s);
-        return code | (x < 0.0f ? 8u : 0u);
+        off = fmaxf(off, __builtin_fabsf(y - n));
+        return fminf(n + base, 7.0f);
     } else {
-        float n = __builtin_rintf(q);
-        if (__builtin_fabsf(__builtin_fabsf(q - n) - 0.5f) < kNear) n = nearest_quotient(x, s);
-        return (uint32_t)fminf(fmaxf(n + z, 0.0f), 15.0f);
+        // the integer nearest to x / s + z; z is whole, and ties are left to the exact code
+        const float y = fmaf(x, inv, z), n = __builtin_rintf(y);
+        off = fmaxf(off, __builtin_fabsf(y - n));
+        return fminf(n, 15.0f);
     }
+}
+template <int QT>
+__device__ __forceinline__ uint32_t exact_code(float x, float s, float z) {
+    if constexpr (QT == DT_FP4) return nearest_e2m1(__builtin_fabsf(x), s) | (x < 0.0f ? 8u : 0u);
+    else return (uint32_t)fminf(fmaxf(nearest_quotient(x, s) + z, 0.0f), 15.0f);
 }
 
 // Eight codes of a lane's elements e0 .. e0 + 7, those at and past K zero.
 template <int QT>
-__device__ __forceinline__ uint32_t codes_of(const float (&x)[8], float s, float z, int e0, int K) {
-    if (s == 0.0f) {   // every code is z
-        uint32_t w = (uint32_t)z * 0x11111111u;
-        if (e0 + 8 > K) w = e0 >= K ? 0u : w & ((1u << (4 * (K - e0))) - 1u);
-        return w;
-    }
-    const float inv = 1.0f / s;
-    uint32_t w = 0;
+__device__ __forceinline__ uint32_t codes_of(const float (&x)[8], float s, float inv, float z, int e0, int K) {
+    uint32_t w = (uint32_t)z * 0x11111111u;   // s == 0: every code is z
+    if (s != 0.0f) {
+        float off = 0.0f;
+        uint32_t even = 0, odd = 0;   // four codes each, a byte a code; the conversion stops at 0
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const uint32_t c = code_of<QT>(x[i], s, inv, z);
-        if (e0 + i < K) w |= c << (4 * i);
+        for (int i = 0; i < 4; ++i) {
+            even = __builtin_amdgcn_cvt_pk_u8_f32(code_of<QT>(x[2 * i], inv, z, off), i, even);
+            odd = __builtin_amdgcn_cvt_pk_u8_f32(code_of<QT>(x[2 * i + 1], inv, z, off), i, odd);
+        }
+        w = even | (odd << 4);
+        if constexpr (QT == DT_FP4) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) w |= x[i] < 0.0f ? 8u << (4 * i) : 0u;
+        }
+        if (!(off <= 0.5f - kNear)) {   // some quotient is too near a middle to tell
+            w = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) w |= exact_code<QT>(x[i], s, z) << (4 * i);
+        }
     }
+    if (e0 + 8 > K) w = e0 >= K ? 0u : w & ((1u << (4 * (K - e0))) - 1u);
     return w;
 }
 
@@ -123,7 +177,7 @@ __device__ __forceinline__ uint32_t codes_of(const float (&x)[8], float s, float
 constexpr int kRows = 32, kSteps = kRows / 4, kCols = 512;
 
 template <int WT, int QT, bool SYM, int GROUP>
-__global__ __launch_bounds__(256) void w4_quantize_kernel(W4QuantParams p, int64_t units, int blocks) {
+__global__ __launch_bounds__(256, 4) void w4_quantize_kernel(W4QuantParams p, int64_t units, int blocks) {
     constexpr int LANES = GROUP / 8, PER = kCols / GROUP;   // lanes of a group, groups of a unit's row
     __shared__ uint32_t words[PER][kRows];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -137,28 +191,17 @@ __global__ __launch_bounds__(256) void w4_quantize_kernel(W4QuantParams p, int64
 #pragma unroll
         for (int st = 0; st < kSteps; ++st) {
             const int64_t row = row0 + wave * kSteps + st;
-            load8<WT>(x[st], p.W + row * p.w_pitch, e0, row < p.N ? p.K : 0);
+            load8<WT, true>(x[st], p.W + row * p.w_pitch, e0, row < p.N ? p.K : 0);
         }
 #pragma unroll
         for (int st = 0; st < kSteps; ++st) {
             const int64_t row = row0 + wave * kSteps + st;
-            Range r;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) r.add(x[st][i]);
-            r.top = reduce_lanes<LANES>(r.top, [](uint32_t a, uint32_t b) { return max(a, b); });
-            if constexpr (QT != DT_FP4 && !SYM) {
-                const auto fmin_ = [](uint32_t a, uint32_t b) {
-                    return __builtin_bit_cast(uint32_t, fminf(__builtin_bit_cast(float, a), __builtin_bit_cast(float, b)));
-                };
-                const auto fmax_ = [](uint32_t a, uint32_t b) {
-                    return __builtin_bit_cast(uint32_t, fmaxf(__builtin_bit_cast(float, a), __builtin_bit_cast(float, b)));
-                };
-                r.lo = __builtin_bit_cast(float, reduce_lanes<LANES>(__builtin_bit_cast(uint32_t, r.lo), fmin_));
-                r.hi = __builtin_bit_cast(float, reduce_lanes<LANES>(__builtin_bit_cast(uint32_t, r.hi), fmax_));
-            }
-            float s, z;
-            const uint32_t word = scale_word<QT, SYM>(r, s, z);
-            const uint32_t q = codes_of<QT>(x[st], s, z, e0, p.K);
+            Range<SYM> r;
+            r.add(x[st]);
+            r.template gather<LANES>();
+            float s, inv, z;
+            const uint32_t word = scale_word<QT, SYM>(r, s, inv, z);
+            const uint32_t q = codes_of<QT>(x[st], s, inv, z, e0, p.K);
             if (row < p.N && e0 < kp) *reinterpret_cast<uint32_t *>(p.codes + row * p.pitch + e0 / 2) = q;
             if (lane % LANES == 0) words[lane / LANES][wave * kSteps + st] = word;
         }
@@ -174,43 +217,40 @@ __global__ __launch_bounds__(256) void w4_quantize_kernel(W4QuantParams p, int64
 
 template <int WT, int QT, bool SYM>
 __global__ __launch_bounds__(256) void w4_quantize_rows_kernel(W4QuantParams p) {
-    __shared__ float lo[4], hi[4];
-    __shared__ uint32_t top[4];
+    __shared__ uint32_t hi[4], neg[4];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int kp = (p.K + 31) / 32 * 32;
     for (int64_t row = blockIdx.x; row < p.N; row += gridDim.x) {
         const uint8_t *src = p.W + row * p.w_pitch;
-        Range r;
+        Range<SYM> r;
         for (int64_t e0 = threadIdx.x * 8; e0 < p.K; e0 += 256 * 8) {
             float x[8];
             load8<WT>(x, src, e0, p.K);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) r.add(x[i]);
+            const uint32_t before = r.hi;
+            r.add(x);
+            r.hi = max(r.hi, before);   // a value that was not finite stays
         }
         for (int d = 1; d < 64; d *= 2) {
-            r.lo = fminf(r.lo, __shfl_xor(r.lo, d));
-            r.hi = fmaxf(r.hi, __shfl_xor(r.hi, d));
-            r.top = max(r.top, (uint32_t)__shfl_xor((int)r.top, d));
+            r.hi = max(r.hi, (uint32_t)__shfl_xor((int)r.hi, d));
+            r.neg = max(r.neg, (uint32_t)__shfl_xor((int)r.neg, d));
         }
         if (lane == 0) {
-            lo[wave] = r.lo;
             hi[wave] = r.hi;
-            top[wave] = r.top;
+            neg[wave] = r.neg;
         }
         __syncthreads();
         for (int w = 0; w < 4; ++w) {
-            r.lo = fminf(r.lo, lo[w]);
-            r.hi = fmaxf(r.hi, hi[w]);
-            r.top = max(r.top, top[w]);
+            r.hi = max(r.hi, hi[w]);
+            r.neg = max(r.neg, neg[w]);
         }
         __syncthreads();   // before the next row's values
-        float s, z;
-        const uint32_t word = scale_word<QT, SYM>(r, s, z);
+        float s, inv, z;
+        const uint32_t word = scale_word<QT, SYM>(r, s, inv, z);
         if (threadIdx.x == 0) p.words[row] = word;
         for (int64_t e0 = threadIdx.x * 8; e0 < kp; e0 += 256 * 8) {
             float x[8];
             load8<WT>(x, src, e0, p.K);
-            *reinterpret_cast<uint32_t *>(p.codes + row * p.pitch + e0 / 2) = codes_of<QT>(x, s, z, (int)e0, p.K);
+            *reinterpret_cast<uint32_t *>(p.codes + row * p.pitch + e0 / 2) = codes_of<QT>(x, s, inv, z, (int)e0, p.K);
         }
     }
 }
