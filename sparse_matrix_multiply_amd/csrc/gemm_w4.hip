@@ -10,10 +10,14 @@
 //
 // A workgroup owns 16 columns of D and all rows (up to 32); its WK waves split K
 // into contiguous ranges of chunks of 256 elements: of a weight row one 128-byte
-// line, of A 512 bytes.  Each wave copies its chunks straight into a private ring
-// of LDS slots, NSLOT chunks ahead, in whole lines, and reads the fragments back
-// from there; no barrier until the partial tiles are added up in wave order.  The
-// time is that of streaming the codes from HBM.
+// line, of A 512 bytes.  Each wave copies a chunk straight into LDS, in whole
+// lines, reads the fragments from there into registers and has the next chunk
+// copied while it multiplies; no barrier until the partial tiles are added up in
+// wave order.  The time is that of streaming the codes from HBM, and what covers
+// the latency is many workgroups per compute unit rather than many chunks per
+// wave: with one chunk per wave in LDS instead of two to four, 1 x 8192 x 8192 (U4,
+// groups of 128) takes 9.0 us instead of 13.1 (4.0 TB/s), 16 rows 12.1 instead of
+// 15.9, 4 x 8192 x 32768 (E2M1, groups of 32) 38 instead of 50 (4.4 TB/s).
 #include "gemm_tiled.h"
 #include "w4_operand.h"
 
@@ -27,21 +31,20 @@ __device__ __forceinline__ f32x4 mma16(const i32x4 &a, const i32x4 &b, f32x4 c) 
         return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
 }
 
-// MR rows of A are staged (2, 8, 16 or 32, at least the rows there are); lanes of
+// MR rows of A are staged (2, 4, 8, 16 or 32, at least the rows there are); lanes of
 // further rows read staged ones again, and their results are not stored.
 // GROUP 128 also serves whole rows (every chunk then reads word 0).
-template <int DT, int QT, int GROUP, int MR, int WK, int NSLOT>
+template <int DT, int QT, int GROUP, int MR, int WK>
 __global__ __launch_bounds__(WK * 64) void gemm_w4_rows_kernel(W4Params p) {
     constexpr int MB = MR > 16 ? 2 : 1;
     constexpr int GPC = 256 / GROUP;              // groups of a chunk
     constexpr int SPG = GROUP / 32;               // instruction steps of a group
     constexpr int SI = (GPC * 16 + 63) / 64;      // copy instructions for scale words
     constexpr int W_BYTES = 16 * 128, A_BYTES = MR * 512, SLOT = W_BYTES + A_BYTES + SI * 256;
-    constexpr int IPC = 2 + MR / 2 + SI;          // copy instructions of a chunk
     constexpr int OUTS = MB * 256;
     constexpr int RED = WK * OUTS * 4;
-    constexpr int LDS_BYTES = WK * NSLOT * SLOT > RED ? WK * NSLOT * SLOT : RED;
-    static_assert(LDS_BYTES <= 160 * 1024 && (NSLOT - 1) * IPC < 64, "LDS and counter range");
+    constexpr int LDS_BYTES = WK * SLOT > RED ? WK * SLOT : RED;
+    static_assert(LDS_BYTES <= 80 * 1024, "LDS: at least two workgroups per compute unit");
     __shared__ __attribute__((aligned(16))) uint8_t smem[LDS_BYTES];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r16 = lane & 15, q = lane >> 4;
     const int col0 = blockIdx.x * 16, rows = p.M;
@@ -58,9 +61,9 @@ __global__ __launch_bounds__(WK * 64) void gemm_w4_rows_kernel(W4Params p) {
     const int nfull = p.K / 256, nall = (p.K + 255) / 256;
     const int per = (nall + WK - 1) / WK;
     const int c0 = min(wave * per, nall), c1 = min(c0 + per, nall), c1f = min(c1, nfull);
-    uint8_t *ring = smem + wave * NSLOT * SLOT;
+    uint8_t *slot = smem + wave * SLOT;
 
-    const auto issue_w = [&](int c, uint8_t *slot) {
+    const auto issue_w = [&](int c) {
 #pragma unroll
         for (int j = 0; j < 2; ++j) {   // 8 rows x one line; unit u of row r at u ^ ((r / 2) mod 8)
             const int r = 8 * j + (lane >> 3);
@@ -76,7 +79,7 @@ __global__ __launch_bounds__(WK * 64) void gemm_w4_rows_kernel(W4Params p) {
         }
     };
     // unit u (8 elements) of row r of A sits at unit u ^ (r mod 16): 16 rows' reads of one unit meet 16 bank groups
-    const auto issue_a = [&](int c, uint8_t *slot) {
+    const auto issue_a = [&](int c) {
 #pragma unroll
         for (int j = 0; j < MR / 2; ++j) {
             const int r = 2 * j + (lane >> 5);
@@ -90,7 +93,7 @@ __global__ __launch_bounds__(WK * 64) void gemm_w4_rows_kernel(W4Params p) {
 
     uint32_t wd[8], sw[GPC];
     i32x4 a[8][MB];
-    const auto load = [&](const uint8_t *slot) {
+    const auto load = [&]() {
 #pragma unroll
         for (int v = 0; v < 8; ++v) {   // step v: elements 32 v + 8 q .. + 7 of the chunk
             wd[v] = *reinterpret_cast<const uint32_t *>(slot + r16 * 128 + ((v ^ ((r16 >> 1) & 7)) << 4) + q * 4);
@@ -130,34 +133,29 @@ __global__ __launch_bounds__(WK * 64) void gemm_w4_rows_kernel(W4Params p) {
         }
     };
 
-#pragma unroll
-    for (int i = 0; i < NSLOT; ++i)
-        if (c0 + i < c1f) {
-            issue_w(c0 + i, ring + i * SLOT);
-            issue_a(c0 + i, ring + i * SLOT);
-        }
-    int slot = 0;
+    if (c0 < c1f) {
+        issue_w(c0);
+        issue_a(c0);
+    }
     for (int c = c0; c < c1f; ++c) {
-        uint8_t *at = ring + slot * SLOT;
-        wait_copies<IPC, NSLOT - 1>(min(NSLOT - 1, c1f - 1 - c));   // chunk c has landed
-        load(at);
-        wait_lds();                                                // read before it is copied over
-        if (c + NSLOT < c1f) {
-            issue_w(c + NSLOT, at);
-            issue_a(c + NSLOT, at);
+        wait_vm_lgkm0<0>();   // chunk c has landed
+        load();
+        wait_lds();           // read before it is copied over
+        if (c + 1 < c1f) {
+            issue_w(c + 1);
+            issue_a(c + 1);
         }
         compute();
-        slot = slot + 1 == NSLOT ? 0 : slot + 1;
     }
     if (c0 < c1 && c1 > nfull) {   // the chunk K ends inside: A through registers, zero past K (codes there are finite)
-        issue_w(c1f, ring);
+        issue_w(c1f);
         for (int j = 0; j < MR / 2; ++j) {
             const int r = 2 * j + (lane >> 5), unit = lane & 31, e0 = c1f * 256 + unit * 8;
-            *reinterpret_cast<i32x4 *>(ring + W_BYTES + r * 512 + ((unit ^ (r & 15)) << 4)) =
+            *reinterpret_cast<i32x4 *>(slot + W_BYTES + r * 512 + ((unit ^ (r & 15)) << 4)) =
                 masked_unit<2>(ra, (uint32_t)r * (uint32_t)p.a_pitch + (uint32_t)e0 * 2u, e0, p.K);
         }
         wait_vm_lgkm0<0>();
-        load(ring);
+        load();
         compute();
     }
 
@@ -181,10 +179,11 @@ __global__ __launch_bounds__(WK * 64) void gemm_w4_rows_kernel(W4Params p) {
 template <int DT, int QT, int GROUP>
 static hipError_t launch_rows(const W4Params &p, hipStream_t s) {
     const dim3 grid((p.N + 15) / 16);
-    if (p.M <= 2) hipLaunchKernelGGL((gemm_w4_rows_kernel<DT, QT, GROUP, 2, 8, 4>), grid, dim3(512), 0, s, p);
-    else if (p.M <= 8) hipLaunchKernelGGL((gemm_w4_rows_kernel<DT, QT, GROUP, 8, 8, 2>), grid, dim3(512), 0, s, p);
-    else if (p.M <= 16) hipLaunchKernelGGL((gemm_w4_rows_kernel<DT, QT, GROUP, 16, 4, 3>), grid, dim3(256), 0, s, p);
-    else hipLaunchKernelGGL((gemm_w4_rows_kernel<DT, QT, GROUP, 32, 4, 2>), grid, dim3(256), 0, s, p);
+    if (p.M <= 2) hipLaunchKernelGGL((gemm_w4_rows_kernel<DT, QT, GROUP, 2, 8>), grid, dim3(512), 0, s, p);
+    else if (p.M <= 4) hipLaunchKernelGGL((gemm_w4_rows_kernel<DT, QT, GROUP, 4, 8>), grid, dim3(512), 0, s, p);
+    else if (p.M <= 8) hipLaunchKernelGGL((gemm_w4_rows_kernel<DT, QT, GROUP, 8, 4>), grid, dim3(256), 0, s, p);
+    else if (p.M <= 16) hipLaunchKernelGGL((gemm_w4_rows_kernel<DT, QT, GROUP, 16, 4>), grid, dim3(256), 0, s, p);
+    else hipLaunchKernelGGL((gemm_w4_rows_kernel<DT, QT, GROUP, 32, 4>), grid, dim3(256), 0, s, p);
     return hipGetLastError();
 }
 template <int DT, int QT>
