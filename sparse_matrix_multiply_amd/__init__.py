@@ -448,6 +448,16 @@ _BYTES = {torch.uint8, torch.int8, torch.float8_e4m3fn, torch.float8_e5m2}
 _WORDS = {torch.int32, torch.uint32}
 
 
+def _out(D, C, bias, act, d_type):
+    """_epilogue, short for the types D can have by itself."""
+    if d_type is not None or D.dtype not in OUT_OF or (C is not None and C.dtype is not D.dtype):
+        return _epilogue(D, bias, act, d_type, C)
+    code = OUT_OF[D.dtype]
+    if code == OUT_ACC and bias is None and act == ACT_NONE:
+        return None
+    return Epilogue(code, act, None if bias is None else bias.data_ptr())
+
+
 def _w4(Wq, SW, N, K, group, q_type):
     """The mmac_w4_t of a weight matrix."""
     if Wq.dtype not in _BYTES:
@@ -518,7 +528,7 @@ def gemm_w4(A, Wq, SW, D, group=128, q_type=U4, alpha=1.0, beta=0.0, C=None, a_t
     if bias is not None:
         _bias(bias, N)
     q = _w4(Wq, SW, N, K, group, q_type)
-    ep = _epilogue(D, bias, act, d_type, C)
+    ep = _out(D, C, bias, act, d_type)
     ws, nbytes = _workspace_args(workspace)
     _check(lib().mmac_gemm_w4(_input_type(A, a_type), M, N, K, alpha, A.data_ptr(), _rows_of(A, M, K, "A"),
                               ctypes.byref(q), beta, C.data_ptr() if C is not None else None, ldc, D.data_ptr(), ldd,
@@ -567,7 +577,7 @@ def gemm_mx8_wgrad(dY, Xq, SX, D, alpha=1.0, beta=0.0, C=None, y_type=None, q_ty
     ldd = _rows_of(D, N, K, "D")
     ldc = _rows_of(C, N, K, "C") if C is not None else 0
     tq, ldq, lds = _mx8(Xq, SX, M, K, q_type)
-    ep = _epilogue(D, None, ACT_NONE, d_type, C)
+    ep = _out(D, C, None, ACT_NONE, d_type)
     ws, nbytes = _workspace_args(workspace)
     _check(lib().mmac_gemm_mx8_wgrad(_input_type(dY, y_type), tq, M, N, K, alpha, dY.data_ptr(),
                                      _rows_of(dY, M, N, "dY"), Xq.data_ptr(), ldq, SX.data_ptr(), lds, beta,
