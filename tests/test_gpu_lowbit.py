@@ -192,6 +192,47 @@ def test_gemm_w4_small_integers_exact(q_type, group, M, N, K):
         assert np.array_equal(exact(D), ref), t
 
 
+@pytest.mark.parametrize("t,q_type", [("bf16", R.U4), ("fp16", R.U4), ("bf16", R.FP4)])
+@pytest.mark.parametrize("group", [0, 32, 64, 128])
+@pytest.mark.parametrize("K", [96, 650])
+def test_gemm_w4_widest_tile(t, q_type, group, K):
+    """Enough 128 x 256 tiles (13 x 16) for the widest kernel, ragged at every edge."""
+    M, N = 1601, 3900
+    assert mm.w4_workspace_bytes(M, N, K) == 0
+    A, codes, s, z = w4_problem(M, N, K, group, q_type, t)
+    Wq, SW = w4_tensors(codes, s, z)
+    ref, S = R.gemm_w4(A, codes, s, z, group, q_type)
+    buf, D = guarded(M, N, torch.float32, N + 5, -77.0)
+    mm.gemm_w4(pitched(A, TYPES[t], 1), Wq, SW, D, group=group, q_type=q_type)
+    torch.cuda.synchronize()
+    check_sum(D, ref, S, K, what=f"{t} {q_type} {group} {K}")
+    check_guards(buf, M, N, -77.0)
+
+
+@pytest.mark.parametrize("M,N,K", [(40, 200, 4100), (64, 1000, 2048), (200, 300, 3000)])
+def test_gemm_w4_split_sums_are_deterministic(M, N, K):
+    """With a workspace K is cut into ranges: the same bits on every run, the counters back at zero, and the unsplit
+    call's result within both sums' bounds."""
+    A, codes, s, z = w4_problem(M, N, K, 128, R.U4, "bf16")
+    Wq, SW = w4_tensors(codes, s, z)
+    Ad, ws = pitched(A, torch.bfloat16), mm.w4_workspace(M, N, K)
+    assert ws is not None
+    ref, S = R.gemm_w4(A, codes, s, z, 128, R.U4)
+    first = None
+    for _ in range(4):
+        D = torch.full((M, N), float("nan"), device=dev())
+        mm.gemm_w4(Ad, Wq, SW, D, workspace=ws)
+        check_sum(D, ref, S, K)
+        first = D if first is None else first
+        assert torch.equal(D, first)
+        assert int(ws[:256].view(torch.int32).abs().max()) == 0, "counters"
+    D = torch.empty((M, N), device=dev())
+    mm.gemm_w4(Ad, Wq, SW, D)
+    check_sum(D, ref, S, K)
+    mm.gemm_w4(Ad, Wq, SW, D, workspace=ws[:ws.numel() // 2])      # too small: unsplit
+    check_sum(D, ref, S, K)
+
+
 @pytest.mark.parametrize("M", [3, 20, 140])
 @pytest.mark.parametrize("out", ["fp32", "bf16", "fp16"])
 def test_gemm_w4_epilogue(M, out):
@@ -389,6 +430,28 @@ def test_mx8_dequantize_ragged(t, M, K):
         check_guards(buf, M, K, -77.0)
 
 
+@pytest.mark.parametrize("qx,qw", [("e4m3", "e4m3"), ("e5m2", "e4m3")])
+def test_mx8_matrices_feed_the_block_scaled_product(qx, qw):
+    """What mx8_quantize stores is gemm_mx's operand: their product against the stored values in 64 bits (that
+    instruction's own bound, 2^-13 of the magnitudes' sum, added)."""
+    M, N, K = 70, 100, 320
+    g = rng(qx, qw)
+    X, W = rounded(g.standard_normal((M, K)), torch.bfloat16), rounded(g.standard_normal((N, K)) / 18, torch.bfloat16)
+    parts = []
+    for x, q in ((X, qx), (W, qw)):
+        rows = x.shape[0]
+        Xq = torch.empty((rows, K), dtype=ELEMENTS[q], device=dev())
+        SX = torch.empty((3, -(-rows // 4) * 4), dtype=torch.int32, device=dev())[:, :rows]
+        mm.mx8_quantize(pitched(x, torch.bfloat16), Xq, SX)
+        codes, e = R.mx8_quantize(x, q)
+        parts.append((Xq, SX, R.mx8_values(codes, e, q)))
+    D = torch.empty((M, N), device=dev())
+    (Xq, SX, x), (Wq, SW, w) = parts
+    mm.gemm_mx(Xq, SX, Wq, SW, D)
+    S = np.abs(x) @ np.abs(w).T
+    assert (np.abs(exact(D) - x @ w.T) <= (2 * (K + 32) * R.U32 + 2.0 ** -13) * S).all()
+
+
 # ---- weight gradient -----------------------------------------------------------------------------
 
 def wgrad_problem(M, N, K, t, q, key=0):
@@ -442,6 +505,41 @@ def test_wgrad_of_the_identity_is_the_input(t, q):
     D = exact(D)
     assert np.array_equal(D[~small], want[~small])
     assert (np.abs(D[small]) <= 2.0 ** -126).all()
+
+
+@pytest.mark.parametrize("t,q", [("bf16", "e4m3"), ("bf16", "int8"), ("fp16", "e5m2")])
+@pytest.mark.parametrize("M", [100, 201])
+def test_wgrad_widest_tile(t, q, M):
+    """Enough 256 x 256 tiles (14 x 15) for the widest kernel, ragged at every edge."""
+    N, K = 3500, 3601
+    assert mm.mx8_wgrad_workspace_bytes(M, N, K) == 0
+    Y, codes, e = wgrad_problem(M, N, K, t, q)
+    Xq, SX = put_mx8(codes, e, q)
+    V = R.mx8_values(codes, e, q)[:, :K]
+    slack = (np.abs(Y).T @ np.ones_like(V)) * 2.0 ** -25 if t == "fp16" else 0.0
+    buf, D = guarded(N, K, torch.float32, K + 5, -77.0)
+    mm.gemm_mx8_wgrad(pitched(Y, TYPES[t], 1), Xq, SX, D)
+    torch.cuda.synchronize()
+    check_sum(D, Y.T @ V, np.abs(Y).T @ np.abs(V) + slack / (2 * (M + 32) * R.U32), M)
+    check_guards(buf, N, K, -77.0)
+
+
+@pytest.mark.parametrize("t", ["bf16", "fp16"])
+@pytest.mark.parametrize("q", list(ELEMENTS))
+def test_wgrad_non_finite_values_stay_in_their_columns(t, q):
+    M, N, K = 130, 33, 200
+    Y, codes, e = wgrad_problem(M, N, K, t, q)
+    e[129, 3] = 255
+    bad = np.zeros(K, bool)
+    bad[96:128] = True
+    if q != "int8":
+        codes[5, 170] = 0x7f if q == "e4m3" else 0xfc     # NaN, -infinity
+        bad[170] = True
+    Xq, SX = put_mx8(codes, e, q)
+    D = torch.empty((N, K), device=dev())
+    mm.gemm_mx8_wgrad(pitched(Y, TYPES[t]), Xq, SX, D)
+    D = exact(D)
+    assert not np.isfinite(D[:, bad]).any() and np.isfinite(D[:, ~bad]).all()
 
 
 def test_wgrad_nan_block_and_elements():
