@@ -7,15 +7,26 @@
 // split into three bf16 terms (24 bits together) against -z in three operand
 // slots, the accumulator receives - z * sum a.
 //
-// A workgroup computes BM x 256 of D with waves of 64 x 64 and walks K in chunks of
-// 128.  A's chunk is copied straight into one of three LDS stages and read by all
-// waves; a wave's codes go from memory to its registers (no other wave of its
-// row of waves needs them) one chunk ahead and become operands there.  Per chunk,
-// also one chunk ahead, the waves sum A's rows for the zero points.
-// 64 x 64 is the wave tile at which neither LDS reads of A (64 bytes per cycle and
-// compute unit) nor the conversions (about five vector instructions per
-// matrix instruction, of the seven that fit beside it) fill their pipes, and two
-// waves fit on a SIMD to cover each other's latencies.
+// A workgroup of eight waves computes 128 x 256, 128 x 128 or 64 x 128 of D, a wave 32
+// columns of 128, 64 or 32 rows, and walks K in chunks of 128.  A's chunk and each
+// wave's own codes and scale words are copied straight into LDS, three or four
+// stages; codes become operands in registers, so in the widest tile every code
+// is converted once per workgroup.  While a chunk is multiplied, each wave sums
+// the rows of A that it copied itself for the next one's zero points.
+//
+// A group's sums have to be scaled by vector instructions, 16 per instruction tile
+// and group.  The work of a chunk is therefore cut into phases (one group of K
+// for half of the wave's tiles) with two sets of sums: one phase's are scaled and
+// added while the matrix instructions of the next run.
+//
+// Measured at 2048 x 8192 x 8192 (bf16, groups of 128): U4 309 us (890 TFLOP/s), E2M1 255
+// us (1080), U4 in groups of 32 465 us; a bf16 product of a library at these sizes takes
+// 210 us.  The matrix instructions are busy about 45 % of the cycles; stand-ins
+// that leave a part out ran 17 % (the copies), 8 % (the row sums) and 5 % (the
+// scaling) faster, one with operands that need no conversion no faster, and
+// neither deeper prefetch of the fragments nor 64 x 64 wave tiles (half of
+// the LDS reads, twice the conversions; 349 us against 337) nor one wave per SIMD with
+// 128 x 64 (443 us) changed that.
 #include "gemm_tiled.h"
 #include "w4_operand.h"
 
@@ -49,11 +60,11 @@ void gemm_w4_tiled_kernel(W4Params p) {
     constexpr int BM = 32 * TI * WM, BN = 32 * WN, KC = kW4Chunk, NT = WM * WN * 64;
     constexpr int HT = TI > 1 ? TI / 2 : 1, NH = TI / HT;         // tiles of a phase, phases of a group
     constexpr bool PIPE = NH * (KC / GROUP) % 2 == 0;             // phases alternate between two sets of sums
-    constexpr bool SPLIT = TI < 4;
-    constexpr int GPC = KC / GROUP, SPG = GROUP / 16;            // groups of a chunk, steps of a group
+    constexpr bool SPLIT = TI < 4;                                // the widest tile is only taken where there are tiles enough
+    constexpr int GPC = KC / GROUP, SPG = GROUP / 16;             // groups of a chunk, steps of a group
     constexpr int AP = BM * KC * 2 / 16 / NT;                     // copy instructions of A per chunk: 4 rows each
-    constexpr int SP = (32 * GPC + 63) / 64;                 // of scale words
-    constexpr int LPT = AP + 2 + SP;                         // of a wave's chunk in all
+    constexpr int SP = (32 * GPC + 63) / 64;                      // of scale words
+    constexpr int LPT = AP + 2 + SP;                              // of a wave's chunk in all
     constexpr int LPR = 16 / AP, KL = KC / LPR;                   // lanes per row, elements per lane when rows are summed
     static_assert(LPR <= 8 && KL <= 32 && GROUP % KL == 0, "row sums: up to 8 lanes a row, each within a group");
     // a stage: A's rows, then each wave's codes and scale words
@@ -64,7 +75,7 @@ void gemm_w4_tiled_kernel(W4Params p) {
     constexpr bool TERMS = GROUP > 32;
     constexpr int EXT_BYTES = GPC * BM * (TERMS ? 6 : 4);
     constexpr int LDS_BYTES = STAGES * STAGE + 2 * EXT_BYTES;
-    static_assert(LDS_BYTES <= 160 * 1024 / (NT == 512 ? 1 : 2), "LDS: one workgroup of eight waves or two of four per CU");
+    static_assert(NT == 512 && LDS_BYTES <= 160 * 1024, "eight waves, LDS of one workgroup per compute unit");
     __shared__ __attribute__((aligned(16))) uint8_t smem[LDS_BYTES];
     uint8_t *ext = smem + STAGES * STAGE;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -309,8 +320,7 @@ void gemm_w4_tiled_kernel(W4Params p) {
     for (; c < c1; ++c) chunk(std::false_type{}, c);
     if constexpr (PIPE) add_up(1, NH - 1, scale);
 
-    // ranges joined by the last to arrive, in range order (the partials at device scope, see the tiled GEMM); the
-    // widest tile is only taken where there are tiles enough
+    // ranges joined by the last to arrive, in range order (the partials at device scope, see the tiled GEMM)
     if (SPLIT && p.split.splits > 1) {
         constexpr int TILE_BYTES = BM * BN * 4;
         uint8_t *ws = p.split.partials + (int64_t)tile * p.split.splits * TILE_BYTES;

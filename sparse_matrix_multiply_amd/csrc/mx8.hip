@@ -13,7 +13,9 @@
 // row (1 KiB of a 16-bit type), a wave 8 rows with all their loads in flight.
 // Scale words are stored column-major (one 128-column strip after the other), so
 // the workgroup's 32 words of one strip are one 128-byte line: the quantizer
-// gathers them in LDS and writes whole lines.
+// gathers them in LDS and writes whole lines.  8192^2 bf16 and E4M3: quantized in 43 us
+// (4.7 TB/s), restored in 42 us (4.9 TB/s), where a copy moves 4.9 to 5.5 TB/s; in strips of 128
+// columns of 4 rows per instruction the quantizer took 50 us.
 #include <algorithm>
 
 #include "lowbit.h"

@@ -13,7 +13,9 @@
 // written at a time.  Whole rows: one workgroup per row reads the row twice, the
 // second time from the caches.  A division per element would take longer than the
 // memory does; the product with 1 / s (off by less than 4e-6 for quotients up
-// to 15) decides everywhere but within 1e-5 of a middle.
+// to 15) decides everywhere but within 1e-5 of a middle.  8192^2 bf16 in groups of 128, not
+// symmetric: 56 us (3.0 TB/s; 75 us with the division), bound by the vector
+// instructions, about 13 per element.
 #include <algorithm>
 
 #include "lowbit.h"

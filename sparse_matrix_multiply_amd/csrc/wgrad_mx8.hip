@@ -8,14 +8,21 @@
 // within its range): X is brought to dY's type on its way from memory to LDS, and the
 // sum itself runs on the 32 x 32 matrix instructions with fp32 accumulators.
 //
-// A workgroup owns a BN x 128 tile of D (BN rows: columns of dY) and walks a range of M
-// in chunks of 64 rows.  dY's part of a chunk is copied straight into LDS; X's goes
-// through registers, where its conversion costs one instruction per two
-// elements.  Two LDS stages: while one chunk is multiplied the next is in flight.
-// Fragments are read with the transposing LDS reads, as the summed axis is outermost.
+// A workgroup owns a tile of D (32, 64 or 128 columns of dY by 128 of X, or 256 by 256)
+// and walks a range of M in chunks of 64 rows.  dY's part of a chunk is copied
+// straight into LDS; X's goes through registers, where its conversion costs one
+// instruction per two elements, each element once per tile.  Both are loaded
+// two to four chunks ahead.  Fragments are read with the transposing LDS reads,
+// as the summed axis is outermost, a step ahead of their use.
 //
 // With few tiles M is cut into ranges; each writes its partial tile to the
 // workspace, and the one that arrives last adds them in range order.
+//
+// Measured (bf16 x E4M3): 8190 x 4096 x 4096 with beta = 1 309 us (890 TFLOP/s), 8192^3 1064 us
+// (1033 TFLOP/s); a bf16 product of a library with both operands transposed takes
+// 286 us for the former.  128 x 128 tiles one chunk ahead took 383 and 1440 us.  For few
+// columns of dY the time is that of streaming X: 8192 x 32 x 8192 25 us (2.8 TB/s),
+// 8192 x 64 x 4096 26 us; what they lose against a copy is the join of the ranges.
 #include "gemm_tiled.h"
 #include "lowbit.h"
 
@@ -186,7 +193,8 @@ void gemm_mx8_wgrad_kernel(WgradParams p) {
     const auto chunk = [&](int c, int d) {
         uint8_t *sx = smem_x + ((c - c0) & 1) * X_BYTES;
         const uint8_t *sy = smem + ys * Y_BYTES;
-        // dY's copy of chunk c has landed when at most the D - 1 chunks issued after it are outstanding
+        // dY's copy of chunk c has landed when at most the D - 1 chunks issued after it are outstanding (each is
+        // exactly LPT memory instructions: its copies of dY, and an element and a scale load per unit of X)
         if (c + D <= c1) wait_vm_lgkm0<(D - 1) * LPT>();
         else wait_vm_lgkm0<0>();
         put_x(sx, d);          // its last readers passed the barrier before this one
