@@ -32,14 +32,6 @@
 
 namespace mmac {
 
-template <int DT>
-__device__ __forceinline__ f32x16 mma32(const i32x4 &a, const i32x4 &b, f32x16 c) {
-    if constexpr (DT == DT_BF16)
-        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
-    else
-        return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
-}
-
 // bf16 bits nearest to x, in the low half (finite x of moderate size; NaN stays NaN).
 __device__ __forceinline__ uint32_t bf16_bits(float x) {
     return (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)x);

@@ -141,6 +141,15 @@ __device__ __forceinline__ void load8(float (&x)[8], const uint8_t *row, int64_t
     }
 }
 
+// 32 x 32 tile, 16 elements of the summed axis.
+template <int DT>
+__device__ __forceinline__ f32x16 mma32(const i32x4 &a, const i32x4 &b, f32x16 c) {
+    if constexpr (DT == DT_BF16)
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+    else
+        return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+}
+
 // Lane permutations within 16 lanes (data-parallel primitives, no LDS).
 template <int CTRL>
 __device__ __forceinline__ uint32_t dpp(uint32_t v) {
@@ -156,12 +165,6 @@ __device__ __forceinline__ uint32_t reduce_lanes(uint32_t v, F op) {
     if constexpr (LANES >= 8) v = op(v, dpp<kDppMirror8>(v));
     if constexpr (LANES >= 16) v = op(v, dpp<kDppMirror16>(v));
     return v;
-}
-
-// LDS written by lanes of this wave is visible to its other lanes (a wave's LDS accesses complete in order).
-__device__ __forceinline__ void wave_sync() {
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
 }
 
 // Every LDS access of this wave has completed; outstanding memory loads may remain.

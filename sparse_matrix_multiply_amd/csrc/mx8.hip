@@ -145,7 +145,8 @@ __global__ __launch_bounds__(256) void mx8_dequantize_kernel(Mx8Params p, int64_
         for (int s = 0; s < kSteps; ++s) {
             const int64_t row = row0 + wave * kSteps + s;
             const bool in = row < p.M && e0 < kp;
-            q[s] = in ? *reinterpret_cast<const u32x2 *>(p.Xq + row * p.q_pitch + e0) : u32x2{0, 0};
+            // read past the caches' retention; the result is left in them for who asked for it
+            q[s] = in ? __builtin_nontemporal_load(reinterpret_cast<const u32x2 *>(p.Xq + row * p.q_pitch + e0)) : u32x2{0, 0};
             w[s] = in ? p.SX[strip * p.lds + row] : 0;
         }
 #pragma unroll
@@ -207,7 +208,7 @@ __global__ __launch_bounds__(256) void mx8_dequantize_kernel(Mx8Params p, int64_
 template <class K>
 static hipError_t launch_units(K kernel, const Mx8Params &p, hipStream_t s) {
     const int blocks = (p.K + kCols - 1) / kCols;
-    const int64_t units = (int64_t)blocks * ((p.M + kRows - 1) / kRows);
+    const int64_t units = blocks * (((int64_t)p.M + kRows - 1) / kRows);
     hipLaunchKernelGGL(kernel, dim3((unsigned)std::min<int64_t>(units, 1 << 20)), dim3(256), 0, s, p, units, blocks);
     return hipGetLastError();
 }

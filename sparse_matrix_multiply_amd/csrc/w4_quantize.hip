@@ -264,7 +264,7 @@ static hipError_t launch_as(int group, const W4QuantParams &p, hipStream_t s) {
         return hipGetLastError();
     }
     const int blocks = (p.K + kCols - 1) / kCols;
-    const int64_t units = (int64_t)blocks * ((p.N + kRows - 1) / kRows);
+    const int64_t units = blocks * (((int64_t)p.N + kRows - 1) / kRows);
     const dim3 grid((unsigned)std::min<int64_t>(units, 1 << 20)), block(256);
     switch (group) {
     case 32: hipLaunchKernelGGL((w4_quantize_kernel<WT, QT, SYM, 32>), grid, block, 0, s, p, units, blocks); break;

@@ -28,14 +28,6 @@
 
 namespace mmac {
 
-template <int DT>
-__device__ __forceinline__ f32x16 mma32(const i32x4 &a, const i32x4 &b, f32x16 c) {
-    if constexpr (DT == DT_BF16)
-        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
-    else
-        return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
-}
-
 // XOR of the 16-byte unit number in row r of an LDS tile with U units of 16-bit elements per row: the four rows
 // that one transposing read meets lie in different quarters of the banks.
 template <int U>
@@ -130,7 +122,7 @@ void gemm_mx8_wgrad_kernel(WgradParams p) {
     const int split = unit % p.split.splits, tile = unit / p.split.splits;
     const int first = tile / (4 * p.tiles_k) * 4, gsz = min(p.tiles_n - first, 4), in = tile % (4 * p.tiles_k);
     const int n0 = (first + in % gsz) * BN, k0 = in / gsz * BK;
-    const int chunks = (p.M + MC - 1) / MC;
+    const int chunks = (int)(((int64_t)p.M + MC - 1) / MC);
     const int c0 = split * p.split.per_split, c1 = min(c0 + p.split.per_split, chunks);
     const int y_row = (p.N * 2 + 15) / 16 * 16, kp = (p.K + 31) / 32 * 32;
 
