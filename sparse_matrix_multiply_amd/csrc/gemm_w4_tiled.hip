@@ -21,7 +21,7 @@
 //
 // Measured at 2048 x 8192 x 8192 (bf16, groups of 128): U4 309 us (890 TFLOP/s), E2M1 255
 // us (1080), U4 in groups of 32 465 us; a bf16 product of a library at these sizes takes
-// 210 us.  The matrix instructions are busy about 45 % of the cycles; stand-ins
+// 210 us.  The matrix instructions are busy 42 % of the cycles; stand-ins
 // that leave a part out ran 17 % (the copies), 8 % (the row sums) and 5 % (the
 // scaling) faster, one with operands that need no conversion no faster, and
 // neither deeper prefetch of the fragments nor 64 x 64 wave tiles (half of
