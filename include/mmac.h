@@ -246,10 +246,10 @@ mmac_status_t mmac_gemm_sparse24_ep(mmac_dtype_t a_type, mmac_dtype_t b_type,
  * workgroup; the range that finishes a tile last sums the fp32 (int32)
  * partial tiles in range order 0, 1, 2, ... and applies the epilogue, so
  * results are deterministic and independent of timing.
- *   workspace        device memory, 16-byte aligned, or NULL.  Its first
- *                    bytes hold one counter per output tile: they must be
+ *   workspace        device memory, 16-byte aligned, or NULL.  Its first KiB,
+ *                    where the calls count finished output tiles, must be
  *                    zero before the first call that uses the workspace, and
- *                    every call leaves them zero again (zero it once after
+ *                    every call leaves it zero again (zero it once after
  *                    allocating it, e.g. with hipMemset).
  *   workspace_bytes  its size.  If it is smaller than
  *                    mmac_gemm_workspace_bytes(...) for the call (or
@@ -257,7 +257,8 @@ mmac_status_t mmac_gemm_sparse24_ep(mmac_dtype_t a_type, mmac_dtype_t b_type,
  *                    the _ep call.  A negative size is MMAC_ERR_INVALID_ARG;
  *                    a misaligned workspace MMAC_ERR_MISALIGNED.
  * Calls that share a workspace must not run concurrently (different streams)
- * on the same device; calls in one stream may share it.  Results of a split
+ * on the same device; calls in one stream may share it, whatever their sizes
+ * and kinds (the products of mmac_lowbit.h included).  Results of a split
  * call differ from the unsplit call only by floating-point summation order
  * (int8: not at all).  MMAC_SPLITK=<S> in the environment forces S ranges
  * (if the workspace holds them).

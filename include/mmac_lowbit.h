@@ -79,8 +79,9 @@ mmac_status_t mmac_w4_quantize(mmac_dtype_t w_type, int symmetric, int64_t N, in
  * group's sum of a * (n - z) is scaled as a whole and added up in fp32, so the
  * weight itself is never rounded.  U4: that sum is formed as sum a*n - z * sum a
  * (an infinity in A can give NaN where (n - z) * a alone would be infinite).
- *   workspace  as in mmac_gemm_dense_ws (zeroed once, 16-byte aligned, not shared
- *              by calls that may run at the same time); NULL, or smaller than
+ *   workspace  as in mmac_gemm_dense_ws (zeroed once, 16-byte aligned, shared by
+ *              calls of any size and kind, but not by calls that may run at the
+ *              same time); NULL, or smaller than
  *              mmac_gemm_w4_workspace_bytes says: the call runs unsplit.
  */
 mmac_status_t mmac_gemm_w4(mmac_dtype_t a_type, int64_t M, int64_t N, int64_t K, double alpha, const void *A,

@@ -202,14 +202,24 @@ SplitPlan plan_split(int a, int64_t M, int64_t N, int64_t K, bool sparse) {
     return sp;
 }
 
-// Applies a split plan when the workspace holds it; otherwise the unsplit shape.
+__global__ void zero_fill(uint4 *p, int64_t n) {
+    for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < n; i += (int64_t)gridDim.x * blockDim.x)
+        p[i] = uint4{0u, 0u, 0u, 0u};
+}
+
+// Applies a split plan when the workspace holds it; otherwise the unsplit shape.  Only a forced plan has counters
+// past the workspace's first KiB, where other calls may have left partial sums: a fill kernel zeroes those first.
 TileShape apply_split(GemmParams &p, const SplitPlan &sp, int64_t M, int64_t N, bool sparse, void *ws,
-                      int64_t ws_bytes) {
+                      int64_t ws_bytes, void *stream) {
     if (sp.splits < 2 || !ws || ws_bytes < sp.bytes) return pick_shape(M, N, sparse);
     p.splits = sp.splits;
     p.kt_per_split = (int)sp.kt_per_split;
     p.counters = static_cast<uint32_t *>(ws);
     p.partials = static_cast<uint8_t *>(ws) + sp.counter_bytes;
+    if (sp.counter_bytes > kSplitCounterBytes)
+        hipLaunchKernelGGL(zero_fill, dim3(256), dim3(256), 0, static_cast<hipStream_t>(stream),
+                           reinterpret_cast<uint4 *>(static_cast<uint8_t *>(ws) + kSplitCounterBytes),
+                           (sp.counter_bytes - kSplitCounterBytes) / 16);
     const int tm = tile_rows(sp.shape), tn = tile_cols(sp.shape);
     p.tiles_m = (int)((M + tm - 1) / tm);
     p.tiles_n = (int)((N + tn - 1) / tn);
@@ -254,11 +264,6 @@ mmac_status_t compress_call(mmac_dtype_t a_type, int64_t M, int64_t K, const voi
 // uses the address hipGetSymbolAddress gives for the current device.
 constexpr int64_t kScratchBytes = MMAC_STATIC_SCRATCH_BYTES;
 static __device__ __align__(256) uint8_t scratch[kScratchBytes];
-
-__global__ void zero_fill(uint4 *p, int64_t n) {
-    for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < n; i += (int64_t)gridDim.x * blockDim.x)
-        p[i] = uint4{0u, 0u, 0u, 0u};
-}
 
 constexpr int kMaxDevices = 64;
 struct DeviceScratch {
@@ -335,7 +340,7 @@ mmac_status_t mmac_gemm_dense_ws(mmac_dtype_t a_type, mmac_dtype_t b_type, int64
     GemmParams p = make_params(a_type, M, N, K, alpha, A, lda, B, ldb, beta, C, ldc, D, ldd, ep, shape);
     if (shape == TILE_SKINNY)
         return launched(launch_gemm_skinny(a_type, b_type, p, static_cast<hipStream_t>(stream)));
-    shape = apply_split(p, plan_split(a_type, M, N, K, false), M, N, false, workspace, workspace_bytes);
+    shape = apply_split(p, plan_split(a_type, M, N, K, false), M, N, false, workspace, workspace_bytes, stream);
     return launched(launch_gemm_dense(a_type, b_type, shape, p, static_cast<hipStream_t>(stream)));
 }
 
@@ -386,7 +391,7 @@ mmac_status_t mmac_gemm_sparse24_ws(mmac_dtype_t a_type, mmac_dtype_t b_type, in
     p.idx = idx;
     p.idx_pitch = ldidx;
     const TileShape shape =
-        apply_split(p, plan_split(a_type, M, N, K, true), M, N, true, workspace, workspace_bytes);
+        apply_split(p, plan_split(a_type, M, N, K, true), M, N, true, workspace, workspace_bytes, stream);
     return launched(launch_gemm_sparse(a_type, b_type, shape, p, static_cast<hipStream_t>(stream)));
 }
 

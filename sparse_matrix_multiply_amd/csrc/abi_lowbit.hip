@@ -6,6 +6,7 @@
 #include <cmath>
 #include <cstdint>
 
+#include "launch.h"
 #include "lowbit.h"
 #include "mmac_lowbit.h"
 
@@ -92,25 +93,23 @@ mmac_epilogue_t epilogue_of(const mmac_epilogue_t *ep) {
     return ep ? *ep : mmac_epilogue_t{MMAC_OUT_ACC, MMAC_ACT_NONE, nullptr};
 }
 
-// `chunks` chunks of the summed axis cut into at most `want` ranges, none empty.
+// `chunks` chunks of the summed axis cut into at most `want` ranges, none empty.  The partial tiles lie behind the
+// workspace's first KiB, whose 256 counters are enough for every plan below.
 struct SplitPlan {
     int splits, per_split;
-    int64_t counter_bytes, bytes;
+    int64_t bytes;
 };
 SplitPlan plan(int64_t tiles, int64_t tile_bytes, int64_t chunks, int64_t want) {
-    want = std::max<int64_t>(1, std::min(want, chunks));
+    want = tiles * 4 > kSplitCounterBytes ? 1 : std::max<int64_t>(1, std::min(want, chunks));
     SplitPlan s{};
     s.per_split = (int)std::max<int64_t>(1, (chunks + want - 1) / want);
     s.splits = (int)std::max<int64_t>(1, (chunks + s.per_split - 1) / s.per_split);
-    if (s.splits > 1) {
-        s.counter_bytes = (tiles * 4 + 255) / 256 * 256;
-        s.bytes = s.counter_bytes + tiles * s.splits * tile_bytes;
-    }
+    if (s.splits > 1) s.bytes = kSplitCounterBytes + tiles * s.splits * tile_bytes;
     return s;
 }
 SplitParams apply(const SplitPlan &s, int64_t chunks, void *ws, int64_t ws_bytes) {
     if (s.splits < 2 || !ws || ws_bytes < s.bytes) return SplitParams{1, (int)chunks, nullptr, nullptr};
-    return SplitParams{s.splits, s.per_split, static_cast<uint32_t *>(ws), static_cast<uint8_t *>(ws) + s.counter_bytes};
+    return SplitParams{s.splits, s.per_split, static_cast<uint32_t *>(ws), static_cast<uint8_t *>(ws) + kSplitCounterBytes};
 }
 
 // 4-bit products of more than 32 rows: the largest tile that still gives a workgroup to most of the 256 compute
@@ -123,7 +122,7 @@ W4Tile w4_tile(int64_t M, int64_t N) {
     return tiles(W4_128x256) >= 192 ? W4_128x256 : W4_128x128;
 }
 SplitPlan plan_w4(int64_t M, int64_t N, int64_t K) {
-    if (M <= 32 || N == 0 || K == 0) return SplitPlan{1, 1, 0, 0};
+    if (M <= 32 || N == 0 || K == 0) return SplitPlan{1, 1, 0};
     const W4Tile t = w4_tile(M, N);
     const int64_t tiles = ((M + w4_rows(t) - 1) / w4_rows(t)) * ((N + w4_cols(t) - 1) / w4_cols(t));
     const int64_t chunks = (K + kW4Chunk - 1) / kW4Chunk;
@@ -140,9 +139,9 @@ WgradTile wgrad_tile(int64_t N, int64_t K) {
     return ((N + 255) / 256) * ((K + 255) / 256) >= 192 ? WGRAD_256x256 : WGRAD_128x128;
 }
 SplitPlan plan_wgrad(int64_t M, int64_t N, int64_t K) {
-    if (M == 0 || N == 0 || K == 0) return SplitPlan{1, 1, 0, 0};
+    if (M == 0 || N == 0 || K == 0) return SplitPlan{1, 1, 0};
     const WgradTile t = wgrad_tile(N, K);
-    if (t == WGRAD_256x256) return SplitPlan{1, 1, 0, 0};
+    if (t == WGRAD_256x256) return SplitPlan{1, 1, 0};
     const int64_t tiles = ((N + wgrad_rows(t) - 1) / wgrad_rows(t)) * ((K + wgrad_cols(t) - 1) / wgrad_cols(t));
     const int64_t chunks = (M + kWgradChunk - 1) / kWgradChunk;
     return plan(tiles, wgrad_rows(t) * wgrad_cols(t) * 4, chunks, std::min<int64_t>({8, 512 / tiles, chunks / 4}));

@@ -731,6 +731,14 @@ struct TiledGemm {
 #pragma unroll
                     for (int e = 0; e < 4; ++e) acc[i][j][4 * G4 + e] = sum[e];
                 }
+        // The first tile's first partial may begin inside the workspace's first
+        // KiB, where other plans have counters: every thread zeroes what it read there.
+        const int64_t offset = p.partials - reinterpret_cast<uint8_t *>(p.counters);
+        if (tile == 0 && offset + tid * 16 < kSplitCounterBytes) {
+            static_assert(NT * 16 >= kSplitCounterBytes && SLOT_BYTES >= kSplitCounterBytes, "within the first accesses of the first slot");
+            __builtin_amdgcn_s_waitcnt(0x0f70);   // vmcnt(0): read
+            __builtin_amdgcn_raw_buffer_store_b128(i32x4{0, 0, 0, 0}, make_rsrc(tile_ws, SLOT_BYTES), (uint32_t)(tid * 16), 0, kDeviceScope);
+        }
         return true;
     }
 

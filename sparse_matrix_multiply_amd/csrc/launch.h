@@ -6,6 +6,12 @@
 
 namespace mmac {
 
+// Calls of different kinds and sizes may share a split workspace, so its first
+// KiB is zero between calls: there lie the tile counters (at most 256) of every
+// plan that the library picks by itself.  A plan either keeps its partial tiles
+// behind it, or zeroes what they used of it when they have been read.
+constexpr int64_t kSplitCounterBytes = 1024;
+
 // One GEMM as the tiled kernels see it.  Pitches of A/Ac and B are in bytes,
 // of idx in 32-bit words, of C and D in elements.
 struct GemmParams {
@@ -52,9 +58,10 @@ struct GemmParams {
     int tiles_m, tiles_n, group_m;
     // Split-K: K is cut into `splits` ranges of kt_per_split k-tiles (the last
     // range may be shorter) and each (output tile, range) pair is one
-    // workgroup.  counters: one word per output tile, zero before and after
-    // every call; partials: splits fp32 / int32 tiles of BM x BN per output
-    // tile.  splits == 1: one range, counters and partials unused.
+    // workgroup.  counters: the start of the workspace, one word per output
+    // tile, zero before and after every call; partials: splits fp32 / int32
+    // tiles of BM x BN per output tile (see kSplitCounterBytes).  splits == 1:
+    // one range, counters and partials unused.
     int splits, kt_per_split;
     uint32_t *counters;
     uint8_t *partials;

@@ -238,3 +238,16 @@ def test_reference_quantizer_is_within_half_a_step(q_type, symmetric):
     step = s[:, gi] * (1.0 if q_type == R.FP4 else 0.5 if symmetric else 1.0)
     assert (np.abs(V - W) <= step * (1 + 2.0 ** -12)).all()
     assert np.array_equal(R.unpack_codes(R.pack_codes(codes, 9), 100), codes)
+
+
+def test_split_plans_agree_on_where_partial_tiles_begin(L):
+    """Low-bit calls of every size share a workspace: 1 KiB of counters, at most 256, then the partial tiles."""
+    tile = 64 * 128 * 4
+    assert mm.w4_workspace_bytes(64, 4096, 4096) == 1024 + 32 * 8 * tile
+    assert mm.w4_workspace_bytes(64, 11008, 4096) == 1024 + 86 * 2 * tile
+    assert mm.w4_workspace_bytes(100, 512, 2048) == 1024 + 4 * 8 * 2 * tile
+    assert mm.mx8_wgrad_workspace_bytes(2048, 1024, 2048) == 1024 + 128 * 4 * 2 * tile
+    assert mm.mx8_wgrad_workspace_bytes(1024, 1024, 4096) == 1024 + 256 * 2 * 2 * tile
+    for M, N, K in ((33, 1 << 17, 8192), (64, 1 << 15, 512), (128, 1 << 16, 4096), (8192, 1 << 15, 8192)):
+        for n in (mm.w4_workspace_bytes(M, N, K), mm.mx8_wgrad_workspace_bytes(K, M, N)):
+            assert n == 0 or (n - 1024) % (32 * 128 * 4) == 0 and n <= 1024 + 512 * 4 * tile
