@@ -122,7 +122,8 @@ mmac_status_t mmac_mx8_dequantize(mmac_dtype_t q_type, mmac_dtype_t x_type, int6
  * The sum over the M rows is fp32.  X enters the products in dY's type: exact
  * for BF16 (every element times a power of two has at most 8 significant bits;
  * magnitudes below bf16's smallest subnormal round), rounded to binary16 for
- * F16 (exact in 2^-14 .. 65504).  What lies beyond the type's range is infinite.
+ * F16 (exact in 2^-14 .. 65504).  Finite elements beyond the type's range
+ * saturate, as in mmac_mx8_dequantize.
  *   ep         NULL, or d_type with act NONE and bias NULL
  *              (MMAC_ERR_UNSUPPORTED otherwise).
  *   workspace  as in mmac_gemm_dense_ws: M may be cut into ranges whose partial

@@ -7,6 +7,9 @@
 // bits and its scale is a power of two, so the product is exact in bf16 (in fp16
 // within its range): X is brought to dY's type on its way from memory to LDS, and the
 // sum itself runs on the 32 x 32 matrix instructions with fp32 accumulators.
+// Inputs next to the end of dY's type may have been rounded up past it in their 8
+// bits: finite elements saturate, as the dequantizer has them (the check for blocks where that
+// can be takes 1 % of the widest tiles: 8190 x 4096 x 4096 306 -> 310 us).
 //
 // A workgroup owns a tile of D (32, 64 or 128 columns of dY by 128 of X, or 256 by 256)
 // and walks a range of M in chunks of 64 rows.  dY's part of a chunk is copied
@@ -55,6 +58,11 @@ __device__ __forceinline__ i32x4 tr_frag(const uint8_t *tile, int n0, int s, int
     return f;
 }
 
+// The first exponent at which an element of QT can pass DT's largest value: 256, 32768 or (int8) 128 times
+// its power of two is 2^16 (fp16) or 2^128 (bf16).
+template <int DT, int QT>
+constexpr uint32_t kFirstPast = (DT == DT_F16 ? 127 + 16 : 127 + 128) - (QT == DT_E4M3 ? 8 : QT == DT_E5M2 ? 15 : 7);
+
 // Sixteen elements of one block -> sixteen DT values (32 bytes), scaled: two elements per instruction for the fp8 types.
 template <int DT, int QT>
 __device__ __forceinline__ void scaled16(const i32x4 &q, uint32_t e, i32x4 (&o)[2]) {
@@ -92,6 +100,18 @@ __device__ __forceinline__ void scaled16(const i32x4 &q, uint32_t e, i32x4 (&o)[
         }
         o[d >> 1][2 * (d & 1)] = lo;
         o[d >> 1][2 * (d & 1) + 1] = hi;
+    }
+    if (__any(e >= kFirstPast<DT, QT>)) {   // infinities that are not the element's own: the value before
+        constexpr uint32_t kInf = DT == DT_F16 ? 0x7c00u : 0x7f80u;
+#pragma unroll
+        for (int d = 0; d < 4; ++d)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t element = (uint32_t)q[d] >> (8 * i), up = 16 * (i & 1);
+                const uint32_t w = (uint32_t)o[d >> 1][2 * (d & 1) + i / 2];
+                const bool own = QT == DT_E5M2 && (element & 0x7fu) == 0x7cu;
+                if (((w >> up) & 0x7fffu) == kInf && !own) o[d >> 1][2 * (d & 1) + i / 2] = (int)(w - (1u << up));
+            }
     }
 }
 

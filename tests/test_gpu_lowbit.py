@@ -767,3 +767,65 @@ def test_matrices_beyond_four_gib():
         bound = 4 * (K + 32) * R.U32 * 32 * (A.double().abs() @ W.double().abs().t())
         assert ((D[:, -last:].double() - ref).abs() <= bound).all()
         assert (D[:, :-last] == 0).all()
+
+
+# ---- finite elements past dY's type ----------------------------------------------------------------
+
+@pytest.mark.parametrize("t", ["bf16", "fp16"])
+@pytest.mark.parametrize("q", list(ELEMENTS))
+def test_wgrad_reads_what_the_dequantizer_restores(t, q):
+    """dY = 1 on the diagonal, every finite code with every exponent: D is what mx8_dequantize gives in dY's type, at
+    its ends too (finite elements saturate)."""
+    codes, e = all_values(q)
+    codes = np.where(np.isfinite(R.mx8_values(codes, np.full_like(e, 127), q)), codes, 0)
+    e = np.where(e == 255, 127, e)
+    want = finite_rounded(R.mx8_values(codes, e, q), TYPES[t])
+    Xq, SX = put_mx8(codes, e, q)
+    X, D = torch.empty((256, 256), dtype=TYPES[t], device=dev()), torch.empty((256, 256), device=dev())
+    mm.mx8_dequantize(Xq, SX, X)
+    mm.gemm_mx8_wgrad(torch.eye(256, dtype=TYPES[t], device=dev()), Xq, SX, D)
+    assert np.array_equal(exact(X), want)
+    D = exact(D)
+    small = np.abs(want) < 2.0 ** -126                     # fp32 subnormals may be flushed
+    assert np.array_equal(D[~small], want[~small])
+    assert (np.abs(D[small]) <= 2.0 ** -126).all()
+
+
+@pytest.mark.parametrize("t", ["bf16", "fp16"])
+@pytest.mark.parametrize("q", list(ELEMENTS))
+@pytest.mark.parametrize("N", [1, 40, 200])
+def test_wgrad_saturates_next_to_infinities_and_nan(t, q, N):
+    """One row: each column of D is dY times one element.  Blocks at the border of the type's range and past it, every
+    code in each; infinities and NaN of the element type, and of a block (e = 255), stay."""
+    border = {"e4m3": {"fp16": 135, "bf16": 247}, "e5m2": {"fp16": 128, "bf16": 240}, "int8": {"fp16": 136, "bf16": 248}}[q][t]
+    exps = np.array([127, border - 1, border, border + 1, 254, 255])
+    K = 256 * len(exps)
+    codes = np.tile(np.arange(256), len(exps))[None]
+    codes = codes.astype(np.int8).astype(np.int64) if q == "int8" else codes
+    e = np.repeat(exps, 8)[None]
+    v = finite_rounded(R.mx8_values(codes, e, q), TYPES[t])
+    Xq, SX = put_mx8(codes, e, q)
+    y = 2.0 ** -np.arange(N)[None] * (-1.0) ** np.arange(N) if N <= 2 else 2.0 ** -(np.arange(N)[None] % 5) * (-1.0) ** np.arange(N)
+    D = torch.empty((N, K), device=dev())
+    mm.gemm_mx8_wgrad(pitched(y, TYPES[t]), Xq, SX, D, workspace=mm.mx8_wgrad_workspace(1, N, K))
+    with np.errstate(invalid="ignore"):
+        assert np.array_equal(exact(D), y.T @ v if np.isfinite(v).all() else y.T * v, equal_nan=True)
+
+
+@pytest.mark.parametrize("q", list(ELEMENTS))
+def test_wgrad_of_the_largest_fp16_activations_is_finite(q):
+    """fp16 inputs up to 65504 round up to 65536 in 8 bits; the gradient sees 65504 there, in the widest tiles too."""
+    M, N, K = 70, 3500, 3601
+    g = rng(q)
+    X = g.choice([-65504.0, 65504.0, 63488.0, 61440.0, 1000.0], (M, K))
+    X[:, ::7] = 65504.0
+    Xq = torch.empty((M, -(-K // 32) * 32), dtype=ELEMENTS[q], device=dev())
+    SX = torch.empty((-(-K // 128), M), dtype=torch.int32, device=dev())
+    mm.mx8_quantize(pitched(X, torch.float16), Xq, SX)
+    codes, e = R.mx8_quantize(X, q)
+    V = np.clip(R.mx8_values(codes, e, q)[:, :K], -65504, 65504)
+    assert (np.abs(R.mx8_values(codes, e, q)) > 65504).any()
+    Y = rounded(g.standard_normal((M, N)), torch.float16)
+    D = torch.empty((N, K), device=dev())
+    mm.gemm_mx8_wgrad(pitched(Y, torch.float16), Xq, SX, D)
+    check_sum(D, Y.T @ V, np.abs(Y).T @ np.abs(V), M)
