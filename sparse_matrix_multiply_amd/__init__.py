@@ -449,10 +449,14 @@ _WORDS = {torch.int32, torch.uint32}
 
 
 def _out(D, C, bias, act, d_type):
-    """_epilogue, short for the types D can have by itself."""
-    if d_type is not None or D.dtype not in OUT_OF or (C is not None and C.dtype is not D.dtype):
+    """_epilogue of the products below, whose sums are floating: without a d_type, D is of a floating type and C of D's."""
+    if d_type is not None:
         return _epilogue(D, bias, act, d_type, C)
-    code = OUT_OF[D.dtype]
+    code = OUT_OF.get(D.dtype)
+    if code is None or D.dtype is torch.int32:
+        raise ValueError(f"D has dtype {D.dtype}; expected float32, bfloat16, float16, float8_e4m3fn or float8_e5m2")
+    if C is not None and C.dtype is not D.dtype:
+        raise ValueError(f"C has dtype {C.dtype}; expected D's, {D.dtype}")
     if code == OUT_ACC and bias is None and act == ACT_NONE:
         return None
     return Epilogue(code, act, None if bias is None else bias.data_ptr())

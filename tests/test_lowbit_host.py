@@ -251,3 +251,22 @@ def test_split_plans_agree_on_where_partial_tiles_begin(L):
     for M, N, K in ((33, 1 << 17, 8192), (64, 1 << 15, 512), (128, 1 << 16, 4096), (8192, 1 << 15, 8192)):
         for n in (mm.w4_workspace_bytes(M, N, K), mm.mx8_wgrad_workspace_bytes(K, M, N)):
             assert n == 0 or (n - 1024) % (32 * 128 * 4) == 0 and n <= 1024 + 512 * 4 * tile
+
+
+def test_outputs_are_floating_and_c_has_their_type():
+    """The sums are fp32: an int32 D would hold their bit patterns, an int32 C would be read as some."""
+    A, dY = torch.zeros((4, 64), dtype=torch.bfloat16), torch.zeros((4, 16), dtype=torch.bfloat16)
+    Wq, SW = torch.zeros((32, 32), dtype=torch.uint8), torch.zeros((1, 32), dtype=torch.int32)
+    Xq, SX = torch.zeros((4, 64), dtype=torch.int8), torch.zeros((1, 4), dtype=torch.int32)
+    for d, c, message in ((torch.int32, None, "D has dtype torch.int32"), (torch.int32, torch.int32, "D has dtype torch.int32"),
+                          (torch.int16, None, "D has dtype torch.int16"), (torch.float64, None, "D has dtype torch.float64"),
+                          (torch.float32, torch.int32, "C has dtype torch.int32"), (torch.bfloat16, torch.float16, "C has dtype torch.float16"),
+                          (torch.float16, torch.float32, "C has dtype torch.float32"), (torch.float32, torch.float32, "in GPU memory")):
+        def pair(rows, cols):
+            return torch.zeros((rows, cols), dtype=d), None if c is None else torch.zeros((rows, cols), dtype=c)
+        D, C = pair(4, 32)
+        with pytest.raises(ValueError, match=message):
+            mm.gemm_w4(A, Wq, SW, D, beta=1.0 if c else 0.0, C=C)
+        D, C = pair(16, 64)
+        with pytest.raises(ValueError, match=message):
+            mm.gemm_mx8_wgrad(dY, Xq, SX, D, beta=1.0 if c else 0.0, C=C)
