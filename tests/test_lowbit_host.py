@@ -270,3 +270,88 @@ def test_outputs_are_floating_and_c_has_their_type():
         D, C = pair(16, 64)
         with pytest.raises(ValueError, match=message):
             mm.gemm_mx8_wgrad(dY, Xq, SX, D, beta=1.0 if c else 0.0, C=C)
+
+
+class Reached(Exception):
+    """A call passed every check of the binding."""
+
+
+@pytest.fixture
+def no_library(monkeypatch):
+    """Host tensors count as device ones, and the library's entries raise Reached: a check that is missing shows."""
+    class Entries:
+        def __getattr__(self, name):
+            def call(*args):
+                raise Reached(name)
+            return call
+    monkeypatch.setattr(mm, "lib", lambda: Entries())
+    monkeypatch.setattr(mm, "_stream_of", lambda stream, *tensors: 0)
+
+
+def bf16(*shape):
+    return torch.zeros(shape, dtype=torch.bfloat16)
+
+
+def u8(*shape):
+    return torch.zeros(shape, dtype=torch.uint8)
+
+
+def i8(*shape):
+    return torch.zeros(shape, dtype=torch.int8)
+
+
+def i32(*shape):
+    return torch.zeros(shape, dtype=torch.int32)
+
+
+# entry -> (arguments that pass, [(changed arguments, the message)])
+BINDING = {
+    "w4_quantize": (lambda: dict(W=bf16(32, 64), Wq=u8(32, 32), SW=i32(1, 32)), [
+        (lambda: dict(Wq=u8(31, 32)), r"Wq has shape \(31, 32\)"), (lambda: dict(Wq=u8(32, 31)), r"Wq has shape \(32, 31\)"),
+        (lambda: dict(Wq=u8(1, 32).expand(32, 32)), "Wq: rows .* overlap"), (lambda: dict(Wq=u8(32, 64)[:, ::2]), "Wq: expected a contiguous"),
+        (lambda: dict(Wq=torch.zeros(32, 32, dtype=torch.int16)), "Wq must hold bytes"), (lambda: dict(SW=i32(0, 32)), r"SW has shape \(0, 32\)"),
+        (lambda: dict(group=32), r"SW has shape \(1, 32\), expected \(2, >= 32\)"), (lambda: dict(SW=i32(1, 31)), r"SW has shape \(1, 31\)"),
+        (lambda: dict(SW=torch.zeros(1, 32)), "SW must hold 32-bit"), (lambda: dict(W=torch.zeros(32, 64, dtype=torch.float64)), "expected a float16, bfloat16"),
+        (lambda: dict(W=bf16(1, 64).expand(32, 64)), "W: rows .* overlap"), (lambda: dict(W=bf16(64, 32).t()), "W: expected a contiguous"),
+        (lambda: dict(w_type=mm.F32), "2-byte elements for type code 10")]),
+    "gemm_w4": (lambda: dict(A=bf16(4, 64), Wq=u8(32, 32), SW=i32(1, 32), D=torch.zeros(4, 32)), [
+        (lambda: dict(Wq=u8(32, 16)), r"Wq has shape \(32, 16\)"), (lambda: dict(Wq=torch.zeros(32, 32, dtype=torch.int16)), "Wq must hold bytes"),
+        (lambda: dict(SW=i32(1, 31)), r"SW has shape \(1, 31\)"), (lambda: dict(SW=torch.zeros(1, 32, dtype=torch.int64)), "SW must hold 32-bit"),
+        (lambda: dict(group=32), r"SW has shape \(1, 32\), expected \(2"), (lambda: dict(D=torch.zeros(4, 31)), r"D has shape \(4, 31\)"),
+        (lambda: dict(D=torch.zeros(3, 32)), r"D has shape \(3, 32\)"), (lambda: dict(D=torch.zeros(1, 32).expand(4, 32)), "D: rows .* overlap"),
+        (lambda: dict(D=torch.zeros(32, 4).t()), "D: expected a contiguous"), (lambda: dict(C=torch.zeros(3, 32), beta=1.0), r"C has shape \(3, 32\)"),
+        (lambda: dict(C=torch.zeros(1, 32).expand(4, 32), beta=1.0), "C: rows .* overlap"), (lambda: dict(bias=torch.zeros(31)), "bias must be"),
+        (lambda: dict(bias=bf16(32)), "bias must be"), (lambda: dict(bias=torch.zeros(64)[::2]), "bias must be"),
+        (lambda: dict(A=i32(4, 64)), "expected a float16, bfloat16"), (lambda: dict(a_type=mm.F32), "2-byte elements for type code 10"),
+        (lambda: dict(A=bf16(1, 64).expand(4, 64)), "A: rows .* overlap"), (lambda: dict(A=bf16(64, 4).t()), "A: expected a contiguous"),
+        (lambda: dict(d_type=mm.OUT_BF16), "D has 4-byte elements"), (lambda: dict(workspace=u8(64, 64)[:, :32]), "workspace must be contiguous")]),
+    "mx8_quantize": (lambda: dict(X=torch.zeros(4, 40), Xq=i8(4, 64), SX=i32(1, 4)), [
+        (lambda: dict(Xq=i8(4, 48)), r"Xq has shape \(4, 48\)"), (lambda: dict(Xq=i8(3, 64)), r"Xq has shape \(3, 64\)"),
+        (lambda: dict(Xq=u8(4, 64)), "Xq must hold"), (lambda: dict(Xq=bf16(4, 64)), "Xq must hold"), (lambda: dict(SX=i32(1, 3)), r"SX has shape \(1, 3\)"),
+        (lambda: dict(SX=i32(0, 4)), r"SX has shape \(0, 4\)"), (lambda: dict(SX=torch.zeros(1, 4, dtype=torch.int16)), "SX must hold 32-bit"),
+        (lambda: dict(X=torch.zeros(4, 40, dtype=torch.float64)), "expected a float16, bfloat16"), (lambda: dict(Xq=i8(1, 64).expand(4, 64)), "Xq: rows .* overlap")]),
+    "gemm_mx8_wgrad": (lambda: dict(dY=bf16(4, 16), Xq=i8(4, 64), SX=i32(1, 4), D=torch.zeros(16, 64)), [
+        (lambda: dict(dY=bf16(3, 16)), r"Xq has shape \(4, 64\), expected \(3"), (lambda: dict(D=torch.zeros(15, 64)), r"D has shape \(15, 64\)"),
+        (lambda: dict(D=torch.zeros(16, 128)), r"Xq has shape \(4, 64\), expected \(4, >= 128\)"), (lambda: dict(C=torch.zeros(16, 63), beta=1.0), r"C has shape \(16, 63\)"),
+        (lambda: dict(Xq=u8(4, 64)), "Xq must hold"), (lambda: dict(SX=i32(1, 3)), r"SX has shape \(1, 3\)"),
+        (lambda: dict(dY=torch.zeros(4, 16, dtype=torch.float64)), "expected a float16, bfloat16"), (lambda: dict(D=torch.zeros(1, 64).expand(16, 64)), "D: rows .* overlap"),
+        (lambda: dict(workspace=u8(64, 64)[:, :32]), "workspace must be contiguous")]),
+}
+BINDING["mx8_dequantize"] = BINDING["mx8_quantize"]
+
+
+@pytest.mark.parametrize("entry", list(BINDING))
+def test_each_check_of_the_binding(entry, no_library):
+    """Arguments that fit reach the library, and each that does not raises its own message before that."""
+    fits, changes = BINDING[entry]
+    with pytest.raises(Reached):
+        getattr(mm, entry)(**fits())
+    for change, message in changes:
+        with pytest.raises(ValueError, match=message):
+            getattr(mm, entry)(**{**fits(), **change()})
+
+
+@pytest.mark.parametrize("entry", list(BINDING))
+def test_the_binding_refuses_host_memory(entry):
+    with pytest.raises(ValueError, match="every tensor must be in GPU memory"):
+        getattr(mm, entry)(**BINDING[entry][0]())
