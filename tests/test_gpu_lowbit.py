@@ -829,3 +829,54 @@ def test_wgrad_of_the_largest_fp16_activations_is_finite(q):
     D = torch.empty((N, K), device=dev())
     mm.gemm_mx8_wgrad(pitched(Y, torch.float16), Xq, SX, D)
     check_sum(D, Y.T @ V, np.abs(Y).T @ np.abs(V), M)
+
+
+# ---- the zero points' term of many rows --------------------------------------------------------------
+
+def bf16_rest(x):
+    """x less its nearest bf16 value."""
+    return x - rounded(x, torch.bfloat16)
+
+
+@pytest.mark.parametrize("t", ["bf16", "fp16"])
+@pytest.mark.parametrize("group", [0, 32, 64, 128])
+@pytest.mark.parametrize("M,N", [(40, 150), (130, 200), (1601, 3900)])
+def test_gemm_w4_long_row_sums_exact(t, group, M, N):
+    """Group sums of A of 19 bits with a large mean, under large zero points: as bf16 terms they need all three.  Four
+    elements of 65280 (8 significant bits) and odd ones up to 255 in each group: sum |a| over K stays below 2^19.2, times
+    15 below 2^24, so that every sum is exact in fp32 and the result must match bit for bit."""
+    width = group if group else 128                 # whole rows are summed in chunks of 128
+    K = 2 * width + 16
+    g = rng(t, group, M, N)
+    A = 2.0 * g.integers(0, 128, (M, K)) + 1
+    for k in range(0, 2 * width, width):
+        for i in range(M):
+            A[i, k + g.permutation(width)[:5]] = 65280, 65280, 65280, 65280, 2      # an odd sum
+    A[::3] *= -1
+    assert np.abs(A).sum(1).max() * 15 < 2 ** 24 and (rounded(A, TYPES[t]) == A).all()
+    for k in range(0, 2 * width, width):            # what the third term is for
+        assert (bf16_rest(bf16_rest(A[:, k:k + width].sum(1))) != 0).mean() > 0.5
+    G = R.n_groups(K, group)
+    codes, z, s = g.integers(0, 16, (N, K)), g.integers(11, 16, (N, G)), 2.0 ** g.integers(-2, 1, (N, G))
+    if group:
+        s[:] = s[:, :1]                             # one scale per row, so that the groups' total is exact too
+    ref, _ = R.gemm_w4(A, codes, s, z, group, R.U4)
+    Wq, SW = w4_tensors(codes, s, z)
+    D = torch.full((M, N), float("nan"), device=dev())
+    mm.gemm_w4(pitched(A, TYPES[t]), Wq, SW, D, group=group, workspace=mm.w4_workspace(M, N, K))
+    assert np.array_equal(exact(D), ref)
+
+
+@pytest.mark.parametrize("q_type", [R.U4, R.FP4])
+@pytest.mark.parametrize("group", [0, 32, 64, 128])
+@pytest.mark.parametrize("M", [1, 20, 40, 130])
+def test_gemm_w4_fp16_subnormals_exact(q_type, group, M):
+    """A of multiples of 2^-24 below fp16's normal range (|a| <= 200 units): sums below 2^24 units, bit for bit."""
+    N, K = 70, 300
+    _, codes, s, z = w4_problem(M, N, K, group, q_type, "fp16", integers=True)
+    A = rng(M, group, q_type).integers(-200, 201, (M, K)) * 2.0 ** -24
+    ref, _ = R.gemm_w4(A, codes, s, z, group, q_type)
+    Wq, SW = w4_tensors(codes, s, z)
+    D = torch.full((M, N), float("nan"), device=dev())
+    mm.gemm_w4(pitched(A, torch.float16), Wq, SW, D, group=group, q_type=q_type, workspace=mm.w4_workspace(M, N, K))
+    assert np.array_equal(exact(D), ref)
