@@ -880,3 +880,81 @@ def test_gemm_w4_fp16_subnormals_exact(q_type, group, M):
     D = torch.full((M, N), float("nan"), device=dev())
     mm.gemm_w4(pitched(A, torch.float16), Wq, SW, D, group=group, q_type=q_type, workspace=mm.w4_workspace(M, N, K))
     assert np.array_equal(exact(D), ref)
+
+
+# ---- paths of large and odd calls ----------------------------------------------------------------------
+
+@pytest.mark.parametrize("N", [20, 60, 150])
+@pytest.mark.parametrize("t,top", [(torch.float8_e4m3fn, 448.0), (torch.float8_e5m2, 57344.0)])
+def test_wgrad_fp8_outputs_saturate(N, t, top):
+    """Small integers, so that the sum is exact and only the output rounds."""
+    M, K = 300, 160
+    g = rng(N, top)
+    X, Y = g.integers(-4, 5, (M, K)).astype(np.float64), g.integers(-4, 5, (M, N)).astype(np.float64)
+    C = rounded(g.integers(-200, 201, (N, K)).astype(np.float64), t)
+    codes, e = R.mx8_quantize(X, "int8")
+    Xq, SX = put_mx8(codes, e, "int8")
+    ref = 64 * (Y.T @ X) + 2 * C
+    assert (np.abs(ref) > top).any() == (top == 448.0)
+    D = torch.from_numpy(C).to(dev()).to(t)
+    mm.gemm_mx8_wgrad(pitched(Y, torch.bfloat16), Xq, SX, D, alpha=64.0, beta=2.0, C=D, workspace=mm.mx8_wgrad_workspace(M, N, K))
+    assert np.array_equal(exact(D), torch.from_numpy(np.clip(ref, -top, top)).float().to(t).double().numpy())
+
+
+@pytest.mark.parametrize("q_type,symmetric", FORMS)
+@pytest.mark.parametrize("bad", [np.nan, np.inf, -np.inf])
+def test_w4_quantize_long_rows_that_hold_non_finite_values(q_type, symmetric, bad):
+    """Rows of several passes of a workgroup (2048 elements each), the value in the first, a middle and the last one."""
+    W = rng(q_type, symmetric, str(bad)).standard_normal((5, 7000))
+    W[0, 3], W[1, 2047], W[2, 3000], W[3, 6999] = bad, bad, bad, bad
+    Wq, SW, W = run_w4_quantize(W, torch.float32, 0, q_type, symmetric)
+    codes, s, z = R.w4_quantize(W, 0, q_type, symmetric)
+    assert np.isnan(s[:4]).all() and np.isfinite(s[4]).all()
+    assert np.array_equal(SW.cpu().numpy(), R.scale_words(s, z))
+    assert np.array_equal(Wq.cpu().numpy(), R.pack_codes(codes))
+
+
+@pytest.mark.parametrize("group", [0, 32, 64, 128])
+def test_gemm_w4_nan_scales_in_the_widest_tile(group):
+    """NaN groups, one row of W in a group that ends short, and non-finite rows of A: nothing else changes."""
+    M, N, K = 1601, 3900, 160
+    A, codes, s, z = w4_problem(M, N, K, group, R.U4, "bf16", integers=True)
+    ref, _ = R.gemm_w4(A, codes, s, z, group, R.U4)
+    s[7, 0] = s[3899, -1] = s[300, s.shape[1] // 2] = np.nan
+    A[130, 159], A[1600, 0] = np.nan, np.inf
+    clean = np.ones((M, N), bool)
+    clean[[130, 1600]] = False
+    clean[:, [7, 300, 3899]] = False
+    Wq, SW = w4_tensors(codes, s, z)
+    D = torch.empty((M, N), device=dev())
+    mm.gemm_w4(pitched(A, torch.bfloat16), Wq, SW, D, group=group)
+    D = exact(D)
+    assert np.array_equal(D[clean], ref[clean])
+    assert not np.isfinite(D[~clean]).any()
+
+
+def test_more_units_than_workgroups():
+    """The grids stop at 2^20 workgroups: what comes after is their second turn.  Rows of 8 elements, 32 per unit (one
+    per unit in the whole-row quantizer)."""
+    d = dev()
+    rows, K = (32 << 20) + 77, 8
+    g = torch.Generator(device=d).manual_seed(11)
+    X = torch.randn((rows, K), generator=g, device=d).to(torch.bfloat16)
+    last = slice(rows - 200, rows)                      # on both sides of the border
+    Xq, SX = torch.zeros((rows, 32), dtype=torch.float8_e4m3fn, device=d), torch.zeros((1, rows), dtype=torch.int32, device=d)
+    mm.mx8_quantize(X, Xq, SX)
+    codes, e = R.mx8_quantize(exact(X[last]), "e4m3")
+    assert np.array_equal(SX[:, last].cpu().numpy(), R.sx_words(e))
+    assert np.array_equal(Xq[last].view(torch.uint8).cpu().numpy(), (codes & 255).astype(np.uint8))
+    back = torch.full((rows, K), float("nan"), dtype=torch.bfloat16, device=d)
+    mm.mx8_dequantize(Xq, SX, back)
+    assert np.array_equal(exact(back[last]), finite_rounded(R.mx8_values(codes, e, "e4m3")[:, :K], torch.bfloat16))
+    assert not back.isnan().any()
+    del Xq, SX, back
+    for group, n in ((32, rows), (0, (1 << 20) + 77)):
+        Wq, SW = torch.zeros((n, 16), dtype=torch.uint8, device=d), torch.zeros((1, n), dtype=torch.int32, device=d)
+        mm.w4_quantize(X[:n], Wq, SW, group=group)
+        codes, s, z = R.w4_quantize(exact(X[n - 200:n]), group, R.U4, False)
+        assert np.array_equal(SW[:, n - 200:].cpu().numpy(), R.scale_words(s, z))
+        assert np.array_equal(Wq[n - 200:].cpu().numpy(), R.pack_codes(codes))
+        assert int((SW == 0).sum()) == 0
