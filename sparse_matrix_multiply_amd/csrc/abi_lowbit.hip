@@ -115,7 +115,7 @@ SplitParams apply(const SplitPlan &s, int64_t chunks, void *ws, int64_t ws_bytes
 // 4-bit products of more than 32 rows: the largest tile that still gives a workgroup to most of the 256 compute
 // units; then, if tiles of 128 columns leave units idle, up to 8 K ranges of at least two chunks.  Measured with U4,
 // groups of 128, N = K = 8192: 64 rows 28 us in 64 x 128 tiles and 4 ranges (60 us in 64 x 256 tiles and 8), 512 rows
-// 104 us in 128 x 128 tiles (111 in 128 x 256 and 2 ranges), 2048 rows 318 us in 128 x 256 tiles.
+// 103 us in 128 x 128 tiles (111 in 128 x 256 and 2 ranges), 2048 rows 312 us in 128 x 256 tiles.
 W4Tile w4_tile(int64_t M, int64_t N) {
     const auto tiles = [&](W4Tile t) { return ((M + w4_rows(t) - 1) / w4_rows(t)) * ((N + w4_cols(t) - 1) / w4_cols(t)); };
     if (M <= 64) return W4_64x128;

@@ -16,8 +16,10 @@
 // wave order.  The time is that of streaming the codes from HBM, and what covers
 // the latency is many workgroups per compute unit rather than many chunks per
 // wave: with one chunk per wave in LDS instead of two to four, 1 x 8192 x 8192 (U4,
-// groups of 128) takes 9.0 us instead of 13.1 (4.0 TB/s), 16 rows 12.1 instead of
-// 15.9, 4 x 8192 x 32768 (E2M1, groups of 32) 38 instead of 50 (4.4 TB/s).
+// groups of 128) takes 8.8 us instead of 13.1 (4.0 TB/s), 16 rows 11.9 instead of
+// 15.9, 4 x 32768 x 8192 (E2M1, groups of 32) 37.5 instead of 50 (4.5 TB/s).  From a few
+// rows on A counts too: every workgroup of 16 columns reads all of it (16 bits an
+// element, 13 x 10250 x 4100: 68 MB in all, from the caches, beside 21 MB of codes).
 #include "gemm_tiled.h"
 #include "w4_operand.h"
 

@@ -19,9 +19,10 @@
 // for half of the wave's tiles) with two sets of sums: one phase's are scaled and
 // added while the matrix instructions of the next run.
 //
-// Measured at 2048 x 8192 x 8192 (bf16, groups of 128): U4 309 us (890 TFLOP/s), E2M1 255
-// us (1080), U4 in groups of 32 465 us; a bf16 product of a library at these sizes takes
-// 210 us.  The matrix instructions are busy 42 % of the cycles; stand-ins
+// Measured at 2048 x 8192 x 8192 (bf16, groups of 128): U4 312 us (880 TFLOP/s), E2M1 254
+// us (1080), U4 in groups of 32 469 us; a bf16 product of a library at these sizes takes
+// 210 us.  The widest U4 tile in groups of 128 needs all 256 registers and keeps three values
+// in scratch, outside of its main loop.  The matrix instructions are busy 42 % of the cycles; stand-ins
 // that leave a part out ran 17 % (the copies), 8 % (the row sums) and 5 % (the
 // scaling) faster, one with operands that need no conversion no faster, and
 // neither deeper prefetch of the fragments nor 64 x 64 wave tiles (half of

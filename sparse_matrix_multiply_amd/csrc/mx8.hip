@@ -10,11 +10,13 @@
 // Both kernels stream, so HBM sets their time.  A lane holds eight elements of
 // a row (16 bytes of a 16-bit type), four lanes a block, sixteen lanes the 128
 // columns of one scale word; an instruction of a wave covers 512 columns of one
-// row (1 KiB of a 16-bit type), a wave 8 rows with all their loads in flight.
+// row (1 KiB of a 16-bit type), a wave 8 rows: in the dequantizer with all their loads
+// in flight, in the quantizer one after the other (each load branches on the row's end
+// and is converted in the branch), so that many waves have to cover the latency.
 // Scale words are stored column-major (one 128-column strip after the other), so
 // the workgroup's 32 words of one strip are one 128-byte line: the quantizer
 // gathers them in LDS and writes whole lines.  8192^2 bf16 and E4M3: quantized in 43 us
-// (4.7 TB/s), restored in 42 us (4.9 TB/s), where a copy moves 4.9 to 5.5 TB/s; in strips of 128
+// (4.7 TB/s), restored in 43 us (4.8 TB/s), where a copy moves 4.9 to 5.5 TB/s; in strips of 128
 // columns of 4 rows per instruction the quantizer took 50 us.
 #include <algorithm>
 

@@ -7,15 +7,20 @@
 // sign of the exact remainder w - q * s (one fused multiply-add rounds once and
 // keeps the sign) decides.
 //
-// The work is a streaming pass, bound by HBM.  Groups of 32 to 128: a lane
-// holds eight elements, 4 to 16 lanes a group, a wave 128 columns of 32 rows; the
+// The work is a streaming pass.  Groups of 32 to 128: a lane holds eight
+// elements, 4 to 16 lanes a group, a wave 512 columns of 8 rows; the
 // scale words (group-major) are gathered in LDS so that 32 consecutive ones are
 // written at a time.  Whole rows: one workgroup per row reads the row twice, the
 // second time from the caches.  A division per element would take longer than the
 // memory does; the product with 1 / s (off by less than 4e-6 for quotients up
-// to 15) decides everywhere but within 1e-5 of a middle.  8192^2 bf16 in groups of 128, not
-// symmetric: 56 us (3.0 TB/s; 75 us with the division), bound by the vector
-// instructions, about 13 per element.
+// to 15) decides everywhere but within 1e-5 of a middle.
+//
+// 8192^2 bf16 in groups of 128, not symmetric: 56 us (3.0 TB/s; 75 us with the
+// division); whole rows 46 us.  A row's load branches on the row's end and is converted
+// in the branch, so it is waited for before the next one is issued: what bounds
+// the time is one load in flight per wave and, behind the loads, the vector
+// instructions (about 13 per element, 22 us of issue), which overlap only with
+// other waves' loads.  The E2M1 forms in groups of 64 and 128 keep one value in scratch.
 #include <algorithm>
 
 #include "lowbit.h"

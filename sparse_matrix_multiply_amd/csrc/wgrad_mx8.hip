@@ -21,11 +21,13 @@
 // With few tiles M is cut into ranges; each writes its partial tile to the
 // workspace, and the one that arrives last adds them in range order.
 //
-// Measured (bf16 x E4M3): 8190 x 4096 x 4096 with beta = 1 309 us (890 TFLOP/s), 8192^3 1064 us
-// (1033 TFLOP/s); a bf16 product of a library with both operands transposed takes
+// Measured (bf16 x E4M3): 8190 x 4096 x 4096 with beta = 1 312 us (880 TFLOP/s), 8192^3 1069 us
+// (1028 TFLOP/s); a bf16 product of a library with both operands transposed takes
 // 286 us for the former.  128 x 128 tiles one chunk ahead took 383 and 1440 us.  For few
-// columns of dY the time is that of streaming X: 8192 x 32 x 8192 25 us (2.8 TB/s),
-// 8192 x 64 x 4096 26 us; what they lose against a copy is the join of the ranges.
+// columns of dY the time is that of streaming X: 8192 x 32 x 8192 26 us (2.7 TB/s),
+// 8192 x 64 x 4096 26 us; what they lose against a copy is the join of the ranges.  In
+// between the partial tiles weigh as much as the operands: 8192 x 256 x 4096 46 us, 64 tiles in 8
+// ranges, 33.5 MB written and read back beside 43 MB of operands and result.
 #include "gemm_tiled.h"
 #include "lowbit.h"
 
