@@ -2,7 +2,7 @@
 
 A workspace is zeroed once and calls in one stream may share it, whatever their shapes: the counters
 of one call must not lie where another one left partial sums.  The products here differ in tile count
-(16 to 324) and in ranges; every ordered pair of them runs through one buffer, with D preset to NaN,
+(4 to 324) and in ranges; every ordered pair of them runs through one buffer, with D preset to NaN,
 and has to give the bits it gives with a workspace of its own, which are within the operator's bound
 of the 64-bit product.
 """
