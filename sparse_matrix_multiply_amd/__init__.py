@@ -1,7 +1,7 @@
 """Python binding of libmmac: tiled dense and 4:2-sparse GEMM for MI355X (gfx950).
 
-Thin ctypes layer over the C ABI in include/mmac.h and include/mmac_lowbit.h, with
-the same entry points.  It only marshals arguments: torch tensors provide device memory and
+Thin ctypes layer over the C ABI in include/mmac.h, mmac_lowbit.h, mmac_mx4.h,
+mmac_norm.h and mmac_grouped.h, with the same entry points.  It only marshals arguments: torch tensors provide device memory and
 the current HIP stream; every step of the computation runs in the library's
 HIP kernels.  If libmmac.so is missing, importing the binding succeeds but the
 first call raises -- there is no fallback path.
@@ -17,6 +17,8 @@ Tensor conventions (element strides; the last dimension must be contiguous):
     4-bit weights   codes N x 16 ceil(K/32) uint8, scale words groups x N int32
     8-bit activations   elements M x 32 ceil(K/32) (float8_e4m3fn, float8_e5m2 or int8),
                scale words ceil(K/128) x M int32
+    4-bit block-scaled rows   M x 16 ceil(K/32) uint8, scale words as above
+    products grouped by expert   B groups x N x K (or K x N), bias groups x N, offsets groups + 1 int32
 """
 import ctypes
 import os
@@ -115,6 +117,23 @@ def lib():
                                           i64, ep, vp, i64, vp]
         L.mmac_gemm_mx8_wgrad_workspace_bytes.restype = i64
         L.mmac_gemm_mx8_wgrad_workspace_bytes.argtypes = [i64, i64, i64]
+        L.mmac_mx4_quantize.restype = i32
+        L.mmac_mx4_quantize.argtypes = [i32, i64, i64, vp, i64, vp, i64, vp, i64, vp]
+        L.mmac_rmsnorm.restype = i32
+        L.mmac_rmsnorm.argtypes = [i32, i32, i32, i64, i64, vp, i64, vp, i64, vp, dbl, vp, i64, vp, i64, vp, i64, vp, vp]
+        L.mmac_rmsnorm_grad.restype = i32
+        L.mmac_rmsnorm_grad.argtypes = [i32, i32, i64, i64, vp, i64, vp, i64, vp, vp, vp, i64, vp, i64, vp, vp, i64, vp]
+        L.mmac_rmsnorm_grad_workspace_bytes.restype = i64
+        L.mmac_rmsnorm_grad_workspace_bytes.argtypes = [i64, i64]
+        L.mmac_gemm_grouped.restype = i32
+        L.mmac_gemm_grouped.argtypes = [i32, i32, i64, i64, i64, i64, dbl, vp, i64, vp, vp, i64, i64, dbl, vp, i64, vp,
+                                        i64, ep, vp]
+        L.mmac_gemm_grouped_mx.restype = i32
+        L.mmac_gemm_grouped_mx.argtypes = [i32, i32, i64, i64, i64, i64, dbl, vp, i64, vp, i64, vp, vp, i64, i64, vp, i64,
+                                           i64, dbl, vp, i64, vp, i64, ep, vp]
+        L.mmac_gemm_grouped_wgrad.restype = i32
+        L.mmac_gemm_grouped_wgrad.argtypes = [i32, i64, i64, i64, i64, dbl, vp, i64, vp, i64, vp, dbl, vp, i64, i64, vp,
+                                              i64, i64, ep, vp]
         L.mmac_status_string.restype = ctypes.c_char_p
         L.mmac_status_string.argtypes = [i32]
         _lib = L
@@ -588,6 +607,204 @@ def gemm_mx8_wgrad(dY, Xq, SX, D, alpha=1.0, beta=0.0, C=None, y_type=None, q_ty
                                      C.data_ptr() if C is not None else None, ldc, D.data_ptr(), ldd,
                                      None if ep is None else ctypes.byref(ep), ws, nbytes,
                                      _stream_of(stream, dY, Xq, SX, C, D, workspace)), "mmac_gemm_mx8_wgrad")
+    return D
+
+
+def mx4_quantize(X, Xq, SX, x_type=None, stream=None):
+    """Rows X (M x K, float16, bfloat16 or float32) to packed FP4 (E2M1) elements Xq (M x 16 ceil(K/32) bytes) and scale
+    words SX (ceil(K/128) x M int32): the operand form of gemm_mx (K % 32 == 0) and of gemm_grouped_mx's weights."""
+    M, K = X.shape
+    if Xq.dtype not in _BYTES:
+        raise ValueError("Xq must hold bytes, two elements each")
+    if SX.dtype not in _WORDS:
+        raise ValueError("SX must hold 32-bit scale words")
+    _check(lib().mmac_mx4_quantize(_input_type(X, x_type), M, K, X.data_ptr(), _rows_of(X, M, K, "X"), Xq.data_ptr(),
+                                   max(_rows_of(Xq, M, (K + 31) // 32 * 16, "Xq", True), 16), SX.data_ptr(),
+                                   _rows_of(SX, (K + 127) // 128, M, "SX", True), _stream_of(stream, X, Xq, SX)),
+           "mmac_mx4_quantize")
+    return Xq, SX
+
+
+# ---- RMS norm (include/mmac_norm.h) --------------------------------------------------------------
+
+def _vector(t, n, name, dtypes=(torch.float32,)):
+    """The address of a contiguous vector of n values."""
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} has dtype {t.dtype}; expected {' or '.join(sorted(str(d) for d in dtypes))}")
+    if t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
+        raise ValueError(f"{name} must be a contiguous vector of {n} values")
+    return t.data_ptr()
+
+
+def _same_type(t, X, name):
+    if t.dtype is not X.dtype:
+        raise ValueError(f"{name} has dtype {t.dtype}; expected {X.dtype}")
+
+
+def rmsnorm(X, w, Y, eps=1e-6, residual=None, H=None, rstd=None, SY=None, stream=None):
+    """Y = h * r * w with h = X (+ residual, rounded to X's type), r = 1 / sqrt(mean(h^2) + eps) per row of X (M x N,
+    float16, bfloat16 or float32); w of X's type or float32.  Y of X's type, or 8-bit elements (M x 32 ceil(N/32),
+    float8_e4m3fn or float8_e5m2) with their scale words SY (ceil(N/128) x M int32), the operand form of gemm_mx, gemm_grouped_mx
+    and gemm_mx8_wgrad.  H (h itself, may be X or residual) and rstd (r, M float32) are written when given."""
+    M, N = X.shape
+    tx = _input_type(X, None)
+    if Y.dtype is X.dtype:
+        ty, ldy, lds = tx, _rows_of(Y, M, N, "Y"), 0
+        if SY is not None:
+            raise ValueError("SY goes with an 8-bit Y")
+    elif Y.dtype is torch.float8_e4m3fn or Y.dtype is torch.float8_e5m2:
+        if SY is None:
+            raise ValueError("an 8-bit Y needs SY")
+        ty, ldy, lds = _mx8(Y, SY, M, N, None)
+    else:
+        raise ValueError(f"Y has dtype {Y.dtype}; expected {X.dtype}, float8_e4m3fn or float8_e5m2")
+    ldr = ldh = 0
+    if residual is not None:
+        _same_type(residual, X, "residual")
+        ldr = _rows_of(residual, M, N, "residual")
+    if H is not None:
+        _same_type(H, X, "H")
+        ldh = _rows_of(H, M, N, "H")
+    at_w = _vector(w, N, "w", (torch.float32, X.dtype))
+    _check(lib().mmac_rmsnorm(tx, _INPUT_OF[w.dtype], ty, M, N, X.data_ptr(), _rows_of(X, M, N, "X"),
+                              residual.data_ptr() if residual is not None else None, ldr, at_w, eps,
+                              H.data_ptr() if H is not None else None, ldh, Y.data_ptr(), ldy,
+                              SY.data_ptr() if SY is not None else None, lds,
+                              _vector(rstd, M, "rstd") if rstd is not None else None,
+                              _stream_of(stream, X, w, Y, residual, H, rstd, SY)), "mmac_rmsnorm")
+    return Y
+
+
+def rmsnorm_grad_workspace_bytes(M, N):
+    """Bytes of workspace rmsnorm_grad needs for dW."""
+    return int(lib().mmac_rmsnorm_grad_workspace_bytes(M, N))
+
+
+def rmsnorm_grad_workspace(M, N, device=None):
+    """A workspace tensor for rmsnorm_grad with dW."""
+    return _workspace_tensor(rmsnorm_grad_workspace_bytes(M, N), device)
+
+
+def rmsnorm_grad(dY, H, w, rstd, dX, dW=None, dH=None, workspace=None, stream=None):
+    """Gradients of rmsnorm from that of Y and the forward pass's h and r: dX (that of X and of the residual, dH added, the
+    gradient that reaches h on the residual stream; dX may be dY or dH) and dW (N float32; needs a
+    workspace, see rmsnorm_grad_workspace())."""
+    M, N = dY.shape
+    for t, name in ((H, "H"), (dX, "dX"), (dH, "dH")):
+        if t is not None:
+            _same_type(t, dY, name)
+    at_w = _vector(w, N, "w", (torch.float32, dY.dtype))
+    ws, nbytes = _workspace_args(workspace)
+    _check(lib().mmac_rmsnorm_grad(_input_type(dY, None), _INPUT_OF[w.dtype], M, N, dY.data_ptr(), _rows_of(dY, M, N, "dY"),
+                                   H.data_ptr(), _rows_of(H, M, N, "H"), at_w, _vector(rstd, M, "rstd"),
+                                   dH.data_ptr() if dH is not None else None,
+                                   _rows_of(dH, M, N, "dH") if dH is not None else 0, dX.data_ptr(),
+                                   _rows_of(dX, M, N, "dX"), _vector(dW, N, "dW") if dW is not None else None, ws, nbytes,
+                                   _stream_of(stream, dY, H, w, rstd, dX, dW, dH, workspace)), "mmac_rmsnorm_grad")
+    return dX
+
+
+# ---- products grouped by expert (include/mmac_grouped.h) -------------------------------------------
+
+def _groups_of(t, groups, rows, cols, name, wider=False):
+    """Checks a groups x rows x cols tensor; returns the strides of its rows and of its groups."""
+    sh = t.shape
+    if len(sh) != 3 or sh[0] != groups or sh[1] != rows or (sh[2] < cols if wider else sh[2] != cols):
+        raise ValueError(f"{name} has shape {tuple(sh)}, expected ({groups}, {rows}, {'>= ' if wider else ''}{cols})")
+    stride, pitch, step = t.stride()
+    width = sh[2]
+    if step != 1 and width > 1:
+        raise ValueError(f"{name}: expected a contiguous last dimension")
+    if pitch < width:
+        if rows > 1:
+            raise ValueError(f"{name}: rows of a {tuple(sh)} tensor with row stride {pitch} overlap")
+        pitch = width
+    if groups > 1 and stride < (rows - 1) * pitch + width:
+        raise ValueError(f"{name}: groups of a {tuple(sh)} tensor with strides {tuple(t.stride())} overlap")
+    return (pitch if pitch > 0 else 1), stride
+
+
+def _offsets(offsets, groups):
+    return _vector(offsets, groups + 1, "offsets", (torch.int32,))
+
+
+def _group_bias(bias, groups, N):
+    if bias is not None and (bias.dtype != torch.float32 or tuple(bias.shape) != (groups, N) or not bias.is_contiguous()):
+        raise ValueError(f"bias must be a contiguous float32 tensor of shape ({groups}, {N})")
+
+
+def gemm_grouped(A, offsets, B, D, trans_b=False, alpha=1.0, beta=0.0, C=None, a_type=None, stream=None, bias=None,
+                 act=ACT_NONE, d_type=None):
+    """For the rows of each group g, offsets[g] .. offsets[g+1] - 1 (int32, in GPU memory): D = round(act(alpha * A @ B[g].T
+    + beta * C + bias[g])), A M x K (float16 or bfloat16), B groups x N x K of the same type.  trans_b: B is
+    groups x K x N and the product is with B[g] itself: with a forward product's weights, the gradient of its input.
+    Rows of no group are neither read nor written.  Epilogue arguments as in gemm_dense, bias groups x N."""
+    M, K = A.shape
+    if B.dim() != 3:
+        raise ValueError(f"B has shape {tuple(B.shape)}, expected one matrix per group")
+    _same_type(B, A, "B")
+    groups, N = B.shape[0], B.shape[2 if trans_b else 1]
+    ldb, stride_b = _groups_of(B, groups, K if trans_b else N, N if trans_b else K, "B")
+    ldd = _rows_of(D, M, N, "D")
+    ldc = _rows_of(C, M, N, "C") if C is not None else 0
+    _group_bias(bias, groups, N)
+    ep = _out(D, C, bias, act, d_type)
+    _check(lib().mmac_gemm_grouped(_input_type(A, a_type), 1 if trans_b else 0, groups, M, N, K, alpha, A.data_ptr(),
+                                   _rows_of(A, M, K, "A"), _offsets(offsets, groups), B.data_ptr(), ldb, stride_b, beta,
+                                   C.data_ptr() if C is not None else None, ldc, D.data_ptr(), ldd,
+                                   None if ep is None else ctypes.byref(ep),
+                                   _stream_of(stream, A, offsets, B, C, D, bias)), "mmac_gemm_grouped")
+    return D
+
+
+def gemm_grouped_mx(A, SA, offsets, B, SB, D, alpha=1.0, beta=0.0, C=None, a_type=None, b_type=None, stream=None,
+                    bias=None, act=ACT_NONE, d_type=None):
+    """gemm_grouped from block-scaled operands: A M x K (float8_e4m3fn or float8_e5m2) with its scale words SA (ceil(K/128)
+    x >= M int32), B groups x N x K of one of these types, or (b_type FP4_E2M1) groups x N x K/2 uint8 of packed pairs,
+    with SB groups x ceil(K/128) x >= N.  K % 32 == 0."""
+    M, K = A.shape
+    if B.dim() != 3:
+        raise ValueError(f"B has shape {tuple(B.shape)}, expected one matrix per group")
+    groups, N = B.shape[0], B.shape[1]
+    ta, tb = _dtype(A, a_type), _dtype(B, b_type) if b_type is not None or B.dtype in DTYPE_OF else None
+    if tb is None or B.dtype not in _BYTES or A.dtype not in _BYTES:
+        raise ValueError(f"A and B must hold 8-bit elements or packed FP4 (b_type), got {A.dtype} and {B.dtype}")
+    per = 2 if tb == FP4_E2M1 else 1
+    ldb, stride_b = _groups_of(B, groups, N, K // per, "B")
+    if SA.dtype not in _WORDS or SB.dtype not in _WORDS:
+        raise ValueError("SA and SB must hold 32-bit scale words")
+    strips = (K + 127) // 128
+    ldsa = _rows_of(SA, strips, M, "SA", True)
+    ldsb, stride_sb = _groups_of(SB, groups, strips, N, "SB", True)
+    ldd = _rows_of(D, M, N, "D")
+    ldc = _rows_of(C, M, N, "C") if C is not None else 0
+    _group_bias(bias, groups, N)
+    ep = _out(D, C, bias, act, d_type)
+    _check(lib().mmac_gemm_grouped_mx(ta, tb, groups, M, N, K, alpha, A.data_ptr(), _rows_of(A, M, K, "A"), SA.data_ptr(),
+                                      ldsa, _offsets(offsets, groups), B.data_ptr(), ldb * per, stride_b * per, SB.data_ptr(),
+                                      ldsb, stride_sb, beta, C.data_ptr() if C is not None else None, ldc, D.data_ptr(), ldd,
+                                      None if ep is None else ctypes.byref(ep),
+                                      _stream_of(stream, A, SA, offsets, B, SB, C, D, bias)), "mmac_gemm_grouped_mx")
+    return D
+
+
+def gemm_grouped_wgrad(dY, X, offsets, D, alpha=1.0, beta=0.0, C=None, y_type=None, stream=None, d_type=None):
+    """Weight gradients of a grouped product: D[g] = alpha * dY[rows of g].T @ X[rows of g] + beta * C[g] (groups x N x K)
+    with dY M x N and X M x K (float16 or bfloat16).  A group without rows gives beta * C[g]."""
+    M, N = dY.shape
+    K = X.shape[1]
+    _same_type(X, dY, "X")
+    if D.dim() != 3:
+        raise ValueError(f"D has shape {tuple(D.shape)}, expected one matrix per group")
+    groups = D.shape[0]
+    ldd, stride_d = _groups_of(D, groups, N, K, "D")
+    ldc, stride_c = _groups_of(C, groups, N, K, "C") if C is not None else (0, 0)
+    ep = _out(D, C, None, ACT_NONE, d_type)
+    _check(lib().mmac_gemm_grouped_wgrad(_input_type(dY, y_type), groups, M, N, K, alpha, dY.data_ptr(),
+                                         _rows_of(dY, M, N, "dY"), X.data_ptr(), _rows_of(X, M, K, "X"),
+                                         _offsets(offsets, groups), beta, C.data_ptr() if C is not None else None, ldc,
+                                         stride_c, D.data_ptr(), ldd, stride_d, None if ep is None else ctypes.byref(ep),
+                                         _stream_of(stream, dY, X, offsets, C, D)), "mmac_gemm_grouped_wgrad")
     return D
 
 

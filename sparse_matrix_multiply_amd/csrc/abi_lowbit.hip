@@ -1,48 +1,17 @@
 // C ABI of the low-bit operands: argument validation on the host, kernel
 // selection, launch on the caller's stream.  The public contract is in
-// include/mmac_lowbit.h.
+// include/mmac_lowbit.h and include/mmac_mx4.h.
 #include <algorithm>
-#include <cfloat>
-#include <cmath>
 #include <cstdint>
 
-#include "launch.h"
+#include "abi_check.h"
 #include "lowbit.h"
 #include "mmac_lowbit.h"
+#include "mmac_mx4.h"
 
 using namespace mmac;
 
 namespace {
-
-constexpr int64_t kMaxDim = 0x7fffffff;               // M, N, K below 2^31
-constexpr int64_t kMaxPitchBytes = (int64_t)1 << 23;
-constexpr int64_t kMaxWords = (((int64_t)1 << 31) - 1) / 4;   // words of a scale array
-
-bool aligned(const void *p, int n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
-bool bad_dim(int64_t n) { return n < 0 || n > kMaxDim; }
-bool is_16bit(int t) { return t == MMAC_F16 || t == MMAC_BF16; }
-bool is_mx8(int t) { return t == MMAC_I8 || t == MMAC_FP8_E4M3 || t == MMAC_BF8_E5M2; }
-bool is_input(int t) { return is_16bit(t) || t == MMAC_F32; }
-int elem_size(int t) { return t == MMAC_F32 ? 4 : is_16bit(t) ? 2 : 1; }
-int out_size(int d_type) { return d_type == MMAC_OUT_ACC ? 4 : d_type <= MMAC_OUT_F16 ? 2 : 1; }
-
-mmac_status_t launched(hipError_t e) { return e == hipSuccess ? MMAC_OK : MMAC_ERR_HIP; }
-
-// A row-major operand of `cols` elements per row: leading dimension, pitch limit, alignment.
-mmac_status_t check_rows(const void *p, int64_t ld, int64_t cols, int es) {
-    if (ld < cols || ld < 1) return MMAC_ERR_INVALID_ARG;
-    if (ld > kMaxPitchBytes / es) return MMAC_ERR_UNSUPPORTED;
-    if (!aligned(p, 16) || (ld * es) % 16) return MMAC_ERR_MISALIGNED;
-    return MMAC_OK;
-}
-
-// A scale array of `rows` rows of ld words, `cols` of them used.
-mmac_status_t check_words(const void *p, int64_t ld, int64_t rows, int64_t cols) {
-    if (ld < cols || ld < 1) return MMAC_ERR_INVALID_ARG;
-    if (rows > 0 && ld > kMaxWords / rows) return MMAC_ERR_UNSUPPORTED;
-    if (!aligned(p, 4)) return MMAC_ERR_MISALIGNED;
-    return MMAC_OK;
-}
 
 int64_t groups_of(int64_t K, int group) { return group == 0 ? 1 : (K + group - 1) / group; }
 
@@ -55,22 +24,6 @@ mmac_status_t check_w4(const mmac_w4_t *q, int64_t N, int64_t K) {
     if (q->pitch > kMaxPitchBytes) return MMAC_ERR_UNSUPPORTED;
     if (!aligned(q->codes, 16) || q->pitch % 16) return MMAC_ERR_MISALIGNED;
     return check_words(q->words, q->ldw, groups_of(K, q->group), N);
-}
-
-// alpha, beta, C, D and the epilogue of a floating product with an M x N output.
-mmac_status_t check_out(int64_t M, int64_t N, double alpha, double beta, const void *C, int64_t ldc, const void *D,
-                        int64_t ldd, const mmac_epilogue_t &ep) {
-    if (ep.d_type < MMAC_OUT_ACC || ep.d_type > MMAC_OUT_BF8_E5M2 || ep.act < MMAC_ACT_NONE || ep.act > MMAC_ACT_RELU)
-        return MMAC_ERR_INVALID_ARG;
-    if ((M > 0 && N > 0 && (!D || (beta != 0.0 && !C))) || ldd < N || ldd < 1 || (beta != 0.0 && (ldc < N || ldc < 1))) return MMAC_ERR_INVALID_ARG;
-    if (!std::isfinite(alpha) || !std::isfinite(beta) || std::fabs(alpha) > (double)FLT_MAX ||
-        std::fabs(beta) > (double)FLT_MAX)
-        return MMAC_ERR_INVALID_ARG;
-    if (C == D && beta != 0.0 && ldc != ldd) return MMAC_ERR_INVALID_ARG;
-    const int es = out_size(ep.d_type);
-    if (ldd > kMaxPitchBytes / es || (beta != 0.0 && ldc > kMaxPitchBytes / es)) return MMAC_ERR_UNSUPPORTED;
-    if (!aligned(D, es) || (beta != 0.0 && !aligned(C, es)) || (ep.bias && !aligned(ep.bias, 4))) return MMAC_ERR_MISALIGNED;
-    return MMAC_OK;
 }
 
 OutParams out_params(double alpha, double beta, const void *C, int64_t ldc, void *D, int64_t ldd,
@@ -87,10 +40,6 @@ OutParams out_params(double alpha, double beta, const void *C, int64_t ldc, void
     o.act = ep.act;
     o.bias = ep.bias;
     return o;
-}
-
-mmac_epilogue_t epilogue_of(const mmac_epilogue_t *ep) {
-    return ep ? *ep : mmac_epilogue_t{MMAC_OUT_ACC, MMAC_ACT_NONE, nullptr};
 }
 
 // `chunks` chunks of the summed axis cut into at most `want` ranges, none empty.  The partial tiles lie behind the
@@ -257,6 +206,19 @@ mmac_status_t mmac_mx8_dequantize(mmac_dtype_t q_type, mmac_dtype_t x_type, int6
     if (st != MMAC_OK || M == 0 || K == 0) return st;
     return launched(launch_mx8_dequantize(q_type, x_type, mx8_params(x_type, M, K, X, ldx, Xq, ldq, SX, lds),
                                           static_cast<hipStream_t>(stream)));
+}
+
+mmac_status_t mmac_mx4_quantize(mmac_dtype_t x_type, int64_t M, int64_t K, const void *X, int64_t ldx, void *Xq,
+                                int64_t pitch, uint32_t *SX, int64_t lds, void *stream) {
+    if (!is_input(x_type)) return MMAC_ERR_UNSUPPORTED;
+    if (bad_dim(M) || bad_dim(K)) return MMAC_ERR_INVALID_ARG;
+    if (M > 0 && K > 0 && (!X || !Xq || !SX)) return MMAC_ERR_INVALID_ARG;
+    mmac_status_t st = check_rows(X, ldx, K, elem_size(x_type));
+    if (st == MMAC_OK) st = check_rows(Xq, pitch, (K + 31) / 32 * 16, 1);
+    if (st == MMAC_OK) st = check_words(SX, lds, (K + 127) / 128, M);
+    if (st != MMAC_OK || M == 0 || K == 0) return st;
+    return launched(launch_mx4_quantize(x_type, mx8_params(x_type, M, K, X, ldx, Xq, pitch, SX, lds),
+                                        static_cast<hipStream_t>(stream)));
 }
 
 mmac_status_t mmac_gemm_mx8_wgrad(mmac_dtype_t y_type, mmac_dtype_t q_type, int64_t M, int64_t N, int64_t K,

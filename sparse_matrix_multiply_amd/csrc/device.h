@@ -308,6 +308,87 @@ struct MmaMX4 {
     }
 };
 
+// Block-scaled 8-bit A with packed FP4 B (format 4), the instruction's mixed form: each operand's fragments as
+// in its own product above (both put the matrix's K order into the instruction's), k-tiles of 128
+// elements, so B's LDS rows are 64 bytes; one scale word per row and k-tile on both sides.
+template <int FA> struct MmaMX84 {
+    static constexpr bool kSparse = false, kScaled = true;
+    static constexpr int kEsize = 1, kElemBitsB = 4, kAFrag = 32, kBFrag = 16, kKStep = 64;
+    static constexpr int kBK = 128;
+    static constexpr int kARowBytes = kBK, kBRowBytes = kBK / 2;
+    static constexpr int kScaleWords = kBK / 128;
+    typedef f32x16 acc_t;
+    typedef float out_t;
+    __device__ __forceinline__ static constexpr int a_unit(int s, int g, int h) { return 4 * s + g + 2 * h; }
+    __device__ __forceinline__ static constexpr int b_unit(int s, int g, int) { return 2 * s + g; }
+    __device__ __forceinline__ static acc_t mma_scaled(const Frag<32> &a, const Frag<16> &b, acc_t c, uint32_t sa,
+                                                       uint32_t sb) {
+        const i32x8 B = {b.v[0], b.v[1], b.v[2], b.v[3], 0, 0, 0, 0};
+        return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(join(a), B, c, FA, 4, 0, (int)sa, 0, (int)sb);
+    }
+};
+
+// The same products for fp32 results.  v_mfma_scale_f32_*_f8f6f4 loses bits below the largest product of an
+// instruction (measured, relative to the result: 1.7e-5 for E4M3 x E4M3, up to 1.8e-5 for E4M3 x FP4 with blocks of different
+// scales): less than an output of 16 bits or fewer rounds away, but an fp32 output would show it.  Here the
+// elements times their scales become bf16, which holds each of them exactly (magnitudes below 2^-126 apart), and
+// the bf16 instructions add exact products in fp32.
+template <int F> struct ExactBf16 {   // format F: 0 = E4M3, 1 = E5M2, 4 = FP4
+    // 32 elements in operand order (8 words, FP4: 4) -> four bf16 operands of eight
+    template <class V>
+    __device__ __forceinline__ static void convert(i32x4 (&o)[4], const V &w, uint32_t exponent) {
+        const float scale = __builtin_bit_cast(float, (exponent & 0xffu) << 23);   // the conversions read the exponent field
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+            if constexpr (F == 4) {
+                const uint32_t x = (uint32_t)w[n];
+                o[n][0] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(x, scale, 0));
+                o[n][1] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(x, scale, 1));
+                o[n][2] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(x, scale, 2));
+                o[n][3] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(x, scale, 3));
+            } else {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint32_t x = (uint32_t)w[2 * n + h];
+                    if constexpr (F == 0) {
+                        o[n][2 * h] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x, scale, false));
+                        o[n][2 * h + 1] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x, scale, true));
+                    } else {
+                        o[n][2 * h] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(x, scale, false));
+                        o[n][2 * h + 1] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(x, scale, true));
+                    }
+                }
+            }
+        }
+    }
+    static __device__ __forceinline__ void convert(i32x4 (&o)[4], const Frag<32> &f, uint32_t e) { convert(o, join(f), e); }
+    static __device__ __forceinline__ void convert(i32x4 (&o)[4], const Frag<16> &f, uint32_t e) { convert(o, f.v, e); }
+};
+template <int FA, int FB> struct MmaMXExact {
+    static constexpr bool kSparse = false, kScaled = true;
+    static constexpr int kEsize = 1, kElemBitsB = FB == 4 ? 4 : 8, kAFrag = 32, kBFrag = FB == 4 ? 16 : 32, kKStep = 64;
+    static constexpr int kBK = 128;
+    static constexpr int kARowBytes = kBK, kBRowBytes = FB == 4 ? kBK / 2 : kBK;
+    static constexpr int kScaleWords = kBK / 128;
+    typedef f32x16 acc_t;
+    typedef float out_t;
+    // lane half g of step s takes elements 64s + 32g .. + 31, the block 2s + g, of A and B alike
+    __device__ __forceinline__ static constexpr int a_unit(int s, int g, int h) { return 4 * s + 2 * g + h; }
+    __device__ __forceinline__ static constexpr int b_unit(int s, int g, int h) {
+        return FB == 4 ? 2 * s + g : 4 * s + 2 * g + h;
+    }
+    __device__ __forceinline__ static acc_t mma_scaled(const Frag<32> &a, const Frag<kBFrag> &b, acc_t c, uint32_t sa,
+                                                       uint32_t sb) {
+        i32x4 x[4], y[4];
+        ExactBf16<FA>::convert(x, a, sa);
+        ExactBf16<FB>::convert(y, b, sb);
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+            c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, x[n]), __builtin_bit_cast(bf16x8, y[n]), c, 0, 0, 0);
+        return c;
+    }
+};
+
 // Block-scaled FP6 (format 2 = E2M3, 3 = E3M2): one 32-element block of
 // packed elements (24 bytes, element e at bits 6e .. 6e+5) per lane, lane half
 // g holding block g of the instruction's 64 K (established on gfx950 with

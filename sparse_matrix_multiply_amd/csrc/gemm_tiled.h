@@ -123,6 +123,10 @@ __device__ __forceinline__ void wait_copies(int n) {
 template <class O, class = void> struct ElemBits { static constexpr int value = 8 * O::kEsize; };
 template <class O> struct ElemBits<O, std::void_t<decltype(O::kElemBits)>> { static constexpr int value = O::kElemBits; };
 
+// The same of B, where it differs from A's (8-bit A with packed FP4 B).
+template <class O, class = void> struct ElemBitsB { static constexpr int value = ElemBits<O>::value; };
+template <class O> struct ElemBitsB<O, std::void_t<decltype(O::kElemBitsB)>> { static constexpr int value = O::kElemBitsB; };
+
 // Operands stored with M (A) or N (B) contiguous instead of K (16- and 8-bit types).
 template <class O, class = void> struct TransOf { static constexpr bool a = false, b = false; };
 template <class O> struct TransOf<O, std::void_t<decltype(O::kTransA)>> {
@@ -197,7 +201,10 @@ struct TiledGemm {
     rsrc_t ra, rb, rx, rsa, rsb;
     acc_t acc[TM][TN];
 
-    __device__ __forceinline__ TiledGemm(const GemmParams &p_) : p(p_) {
+    // Tile (tm, tn) and K range `split` of the product p; row_base: the matrix row of the scale array that row 0 of
+    // p.A has (not zero where p is one group's rows of a larger matrix).
+    __device__ __forceinline__ TiledGemm(const GemmParams &p_, int tm_, int tn_, int split_, int row_base = 0)
+        : p(p_), tm(tm_), tn(tn_), split(split_) {
         const int tid = threadIdx.x;
         lane = tid & 63;
         wave = __builtin_amdgcn_readfirstlane(tid >> 6);   // uniform: LDS bases go straight to M0
@@ -205,26 +212,34 @@ struct TiledGemm {
         l32 = lane & 31;
         wm = wave / WN;
         wn = wave % WN;
-        tile_coords(blockIdx.x, p, tm, tn, split);
         tile = tm * p.tiles_n + tn;
         kt0 = split * p.kt_per_split;
         row0 = tm * BM;
         col0 = tn * BN;
-        const int arows = min(BM, p.M - row0), bcols = min(BN, p.N - col0);
-        if constexpr (TRANS_A) ra = make_rsrc(p.A + row0 * Op::kEsize, (uint32_t)(p.K * p.a_pitch - row0 * Op::kEsize));
-        else ra = make_rsrc(p.A + (int64_t)row0 * p.a_pitch, (uint32_t)(arows * p.a_pitch));
-        if constexpr (TRANS_B) rb = make_rsrc(p.B + col0 * Op::kEsize, (uint32_t)(p.K * p.b_pitch - col0 * Op::kEsize));
-        else rb = make_rsrc(p.B + (int64_t)col0 * p.b_pitch, (uint32_t)(bcols * p.b_pitch));
-        if constexpr (Op::kSparse)
-            rx = make_rsrc(p.idx + (int64_t)row0 * p.idx_pitch, (uint32_t)(arows * p.idx_pitch * 4));
+        set_operands();
         if constexpr (SCALED) {
-            rsa = make_rsrc(p.sa + row0, (uint32_t)((p.scale_rows * p.ldsa - row0) * 4));
+            rsa = make_rsrc(p.sa + row_base + row0, (uint32_t)((p.scale_rows * p.ldsa - row_base - row0) * 4));
             rsb = make_rsrc(p.sb + col0, (uint32_t)((p.scale_rows * p.ldsb - col0) * 4));
         }
 #pragma unroll
         for (int i = 0; i < TM; ++i)
 #pragma unroll
             for (int j = 0; j < TN; ++j) acc[i][j] = acc_t{};
+    }
+
+    // Buffers over this tile's part of A, B and the index words.
+    __device__ __forceinline__ void set_operands() {
+        const int arows = min(BM, p.M - row0), bcols = min(BN, p.N - col0);
+        // strided operands: K rows, of which the last ends with its own last 16-byte unit
+        const auto strided = [&](int64_t pitch, int width, int at) {
+            return p.K > 0 ? (uint32_t)((p.K - 1) * pitch + (int64_t)(width * Op::kEsize + 15) / 16 * 16 - at * Op::kEsize) : 0u;
+        };
+        if constexpr (TRANS_A) ra = make_rsrc(p.A + row0 * Op::kEsize, strided(p.a_pitch, p.M, row0));
+        else ra = make_rsrc(p.A + (int64_t)row0 * p.a_pitch, (uint32_t)(arows * p.a_pitch));
+        if constexpr (TRANS_B) rb = make_rsrc(p.B + col0 * Op::kEsize, strided(p.b_pitch, p.N, col0));
+        else rb = make_rsrc(p.B + (int64_t)col0 * p.b_pitch, (uint32_t)(bcols * p.b_pitch));
+        if constexpr (Op::kSparse)
+            rx = make_rsrc(p.idx + (int64_t)row0 * p.idx_pitch, (uint32_t)(arows * p.idx_pitch * 4));
     }
 
     // Matrix k-tile of step kt of this workgroup's K walk.
@@ -339,7 +354,7 @@ struct TiledGemm {
         constexpr int EB = ElemBits<Op>::value;
         // bytes of A's (compressed) and B's rows before K, in units of kEsize
         const int climit = (Op::kSparse ? p.K / 2 : p.K) * EB / 8 / Op::kEsize;
-        const int blimit = p.K * EB / 8 / Op::kEsize;
+        const int blimit = p.K * ElemBitsB<Op>::value / 8 / Op::kEsize;
 #pragma unroll
         for (int q = 0; q < AP; ++q) {
             const int u = q * 64 + lane;
@@ -1041,18 +1056,11 @@ struct TiledGemm {
     }
 };
 
-// One workgroup per CU: with WM*WN/4 waves on each SIMD every wave may use
-// 512 / (WM*WN/4) registers.
-template <class Op, int BM, int BN, int WM, int WN, int STAGES>
-__global__ __launch_bounds__(WM *WN * 64) __attribute__((amdgpu_waves_per_eu(WM * WN / 4, WM * WN / 4)))
-void gemm_tiled_kernel(GemmParams p) {
-    typedef TiledGemm<Op, BM, BN, WM, WN, STAGES> T;
-    __shared__ __attribute__((aligned(16))) uint8_t smem[T::LDS_BYTES];
-    T t(p);
-    if constexpr (T::SPARE_BYTES > 0) t.spare = smem + T::STAGES * T::STAGE + t.wave * 256;
-
-    // this workgroup's K range: k-tiles [kt0, kt0 + nkt) of the matrix, the
-    // first nk of them whole (a ragged k-tile can only be the matrix's last)
+// The main loop over this workgroup's K range: k-tiles [t.kt0, t.kt0 + nkt) of the matrix, the first nk of
+// them whole (a ragged k-tile can only be the matrix's last).  first: the sums begin here (a folded C is read).
+template <class T, class Op>
+__device__ __forceinline__ void walk_k(T &t, uint8_t *smem, bool first = true) {
+    const GemmParams &p = t.p;
     const int nk_all = p.K / Op::kBK;
     const int nkt_all = nk_all + (p.K > nk_all * Op::kBK ? 1 : 0);
     const int kt_end = min(t.kt0 + p.kt_per_split, nkt_all);
@@ -1067,6 +1075,9 @@ void gemm_tiled_kernel(GemmParams p) {
     if (p.splits == 1 && nkt == nk && nk >= 4) {
         t.rot = (t.tm + t.tn) & 3;
         t.nkr = nk;
+    } else {
+        t.rot = 0;
+        t.nkr = 0x7fffffff;
     }
 
     // prologue: start k-tiles 0 .. AHEAD-1 (and the folded C, whose loads overlap them)
@@ -1077,7 +1088,7 @@ void gemm_tiled_kernel(GemmParams p) {
             else t.fill_masked(smem + s * T::STAGE, s);
         }
     }
-    if (p.fold_c && t.split == 0) t.load_c_into_acc();
+    if (first && p.fold_c && t.split == 0) t.load_c_into_acc();
     // Copies are counted per wave in issue order.  Before using k-tile kt + 1 the
     // copies of the later k-tiles may stay in flight, provided they are all
     // whole k-tiles (the ragged one issues fewer copy instructions); otherwise
@@ -1093,12 +1104,26 @@ void gemm_tiled_kernel(GemmParams p) {
     int kt = 0, cur = 0;
     for (; kt + T::AHEAD < nk; ++kt) {
         t.template iteration<true>(smem, kt, cur, nk, nkt);
-        cur = (cur + 1 == STAGES) ? 0 : cur + 1;
+        cur = (cur + 1 == T::STAGES) ? 0 : cur + 1;
     }
     for (; kt < nkt; ++kt) {
         t.template iteration<false>(smem, kt, cur, nk, nkt);
-        cur = (cur + 1 == STAGES) ? 0 : cur + 1;
+        cur = (cur + 1 == T::STAGES) ? 0 : cur + 1;
     }
+}
+
+// One workgroup per CU: with WM*WN/4 waves on each SIMD every wave may use
+// 512 / (WM*WN/4) registers.
+template <class Op, int BM, int BN, int WM, int WN, int STAGES>
+__global__ __launch_bounds__(WM *WN * 64) __attribute__((amdgpu_waves_per_eu(WM * WN / 4, WM * WN / 4)))
+void gemm_tiled_kernel(GemmParams p) {
+    typedef TiledGemm<Op, BM, BN, WM, WN, STAGES> T;
+    __shared__ __attribute__((aligned(16))) uint8_t smem[T::LDS_BYTES];
+    int tm, tn, split;
+    tile_coords(blockIdx.x, p, tm, tn, split);
+    T t(p, tm, tn, split);
+    if constexpr (T::SPARE_BYTES > 0) t.spare = smem + T::STAGES * T::STAGE + t.wave * 256;
+    walk_k<T, Op>(t, smem);
     if (p.splits > 1 && !t.fixup(reinterpret_cast<uint32_t *>(smem))) return;
     t.epilogue(smem);
 }

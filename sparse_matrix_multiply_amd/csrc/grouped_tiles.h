@@ -1,0 +1,86 @@
+// Grouped products in tiles: the tiled kernel's main loop and epilogue on one group's part of the arrays.
+#pragma once
+
+#include "gemm_tiled.h"
+#include "grouped.h"
+
+namespace mmac {
+
+template <class Op, int BM, int BN, int WM, int WN, int STAGES>
+__global__ __launch_bounds__(WM *WN * 64) __attribute__((amdgpu_waves_per_eu(WM * WN / 4, WM * WN / 4)))
+void gemm_grouped_kernel(GemmParams p, Groups q) {
+    typedef TiledGemm<Op, BM, BN, WM, WN, STAGES> T;
+    __shared__ __attribute__((aligned(16))) uint8_t smem[T::LDS_BYTES];
+    GroupTileAt at;
+    if (!find_group_tile<BM>(q, p.tiles_n, p.group_m, blockIdx.x, at)) return;
+    take_group(p, q, at);
+    if constexpr (T::SCALED) p.sb += at.g * q.sb_stride;
+    T t(p, at.tm, at.tn, 0, at.first);
+    if constexpr (T::SPARE_BYTES > 0) t.spare = smem + T::STAGES * T::STAGE + t.wave * 256;
+    walk_k<T, Op>(t, smem);
+    t.epilogue(smem);
+}
+
+// Weight gradient: the tiles of every group's D, the sum over the group's rows (both operands' K is strided).  A sum
+// over more rows than one buffer descriptor covers is walked in parts, each with descriptors of its own.
+template <class Op, int BM, int BN, int WM, int WN, int STAGES>
+__global__ __launch_bounds__(WM *WN * 64) __attribute__((amdgpu_waves_per_eu(WM * WN / 4, WM * WN / 4)))
+void gemm_grouped_wgrad_kernel(GemmParams p, Groups q) {
+    typedef TiledGemm<Op, BM, BN, WM, WN, STAGES> T;
+    __shared__ __attribute__((aligned(16))) uint8_t smem[T::LDS_BYTES];
+    // contiguous runs of tiles per XCD, as in tile_coords, the groups one after the other
+    const int per = p.tiles_m * p.tiles_n, U = per * q.count, x = blockIdx.x & 7;
+    const int u = x * (U >> 3) + min(x, U & 7) + (int)(blockIdx.x >> 3), g = u / per, in = u - g * per;
+    const int band = in / (p.group_m * p.tiles_n), top = band * p.group_m, high = min(p.tiles_m - top, p.group_m);
+    const int rest = in - band * p.group_m * p.tiles_n;
+    const int first = __builtin_amdgcn_readfirstlane(min(max(q.offsets[g], 0), q.rows));
+    const int end = __builtin_amdgcn_readfirstlane(min(max(q.offsets[g + 1], first), q.rows));
+    p.A += (int64_t)first * p.a_pitch;
+    p.B += (int64_t)first * p.b_pitch;
+    p.D = static_cast<uint8_t *>(p.D) + g * q.d_stride;
+    if (p.use_c) p.C = static_cast<const uint8_t *>(p.C) + g * q.c_stride;
+    int left = end - first;
+    p.K = min(left, q.span);
+    T t(p, top + rest % high, rest / high, 0);
+    walk_k<T, Op>(t, smem);
+    while ((left -= p.K) > 0) {
+        block_barrier();   // every wave is done with the stages
+        p.A += (int64_t)p.K * p.a_pitch;
+        p.B += (int64_t)p.K * p.b_pitch;
+        p.K = min(left, q.span);
+        t.set_operands();
+        walk_k<T, Op>(t, smem, false);
+    }
+    t.epilogue(smem);
+}
+
+template <class Op>
+hipError_t launch_grouped_op(GroupTile tile, const GemmParams &p, const Groups &g, int64_t blocks, hipStream_t s) {
+    const dim3 grid((unsigned)blocks);
+    switch (tile) {
+    case GROUP_64: hipLaunchKernelGGL((gemm_grouped_kernel<Op, 64, 64, 2, 2, 4>), grid, dim3(256), 0, s, p, g); break;
+    case GROUP_128: hipLaunchKernelGGL((gemm_grouped_kernel<Op, 128, 128, 2, 2, 4>), grid, dim3(256), 0, s, p, g); break;
+    case GROUP_128x256: hipLaunchKernelGGL((gemm_grouped_kernel<Op, 128, 256, 2, 4, 3>), grid, dim3(512), 0, s, p, g); break;
+    case GROUP_256:
+        if constexpr (Op::kScaled) return hipErrorInvalidValue;   // no registers left for the scale words
+        else hipLaunchKernelGGL((gemm_grouped_kernel<Op, 256, 256, 2, 4, 2>), grid, dim3(512), 0, s, p, g);
+        break;
+    default: return hipErrorInvalidValue;
+    }
+    return hipGetLastError();
+}
+
+template <class Op>
+hipError_t launch_grouped_wgrad_op(GroupTile tile, const GemmParams &p, const Groups &g, int64_t blocks, hipStream_t s) {
+    const dim3 grid((unsigned)blocks);
+    switch (tile) {
+    case GROUP_64: hipLaunchKernelGGL((gemm_grouped_wgrad_kernel<Op, 64, 64, 2, 2, 4>), grid, dim3(256), 0, s, p, g); break;
+    case GROUP_128: hipLaunchKernelGGL((gemm_grouped_wgrad_kernel<Op, 128, 128, 2, 2, 4>), grid, dim3(256), 0, s, p, g); break;
+    case GROUP_128x256: hipLaunchKernelGGL((gemm_grouped_wgrad_kernel<Op, 128, 256, 2, 4, 3>), grid, dim3(512), 0, s, p, g); break;
+    case GROUP_256: hipLaunchKernelGGL((gemm_grouped_wgrad_kernel<Op, 256, 256, 2, 4, 2>), grid, dim3(512), 0, s, p, g); break;
+    default: return hipErrorInvalidValue;
+    }
+    return hipGetLastError();
+}
+
+}  // namespace mmac

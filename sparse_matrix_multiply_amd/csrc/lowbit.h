@@ -101,6 +101,7 @@ hipError_t launch_gemm_w4_rows(int a_type, int q_type, const W4Params &p, hipStr
 hipError_t launch_gemm_w4_tiled(int a_type, int q_type, const W4Params &p, hipStream_t s);
 hipError_t launch_mx8_quantize(int x_type, int q_type, const Mx8Params &p, hipStream_t s);
 hipError_t launch_mx8_dequantize(int q_type, int x_type, const Mx8Params &p, hipStream_t s);
+hipError_t launch_mx4_quantize(int x_type, const Mx8Params &p, hipStream_t s);   // Xq: packed codes
 hipError_t launch_gemm_mx8_wgrad(int y_type, int q_type, const WgradParams &p, hipStream_t s);
 
 #if defined(__HIPCC__)

@@ -20,55 +20,12 @@
 // columns of 4 rows per instruction the quantizer took 50 us.
 #include <algorithm>
 
-#include "lowbit.h"
+#include "mx_block.h"
 
 namespace mmac {
 
 // A workgroup's unit: 512 columns of 32 rows, 8 rows a wave.
 constexpr int kRows = 32, kSteps = kRows / 4, kCols = 512;
-
-template <int QT> struct Mx8Type;
-template <> struct Mx8Type<DT_E4M3> { static constexpr int top = 8; static constexpr uint32_t frac = 0x600000; };
-template <> struct Mx8Type<DT_E5M2> { static constexpr int top = 15; static constexpr uint32_t frac = 0x600000; };
-template <> struct Mx8Type<DT_I8> { static constexpr int top = 6; static constexpr uint32_t frac = 0x7e0000; };
-
-// Eight scaled values -> eight element bytes.  The conversion instructions round to nearest even and are exact
-// for the values met here (finite, at most the type's largest); a wave that holds a non-finite value takes the
-// bit-level conversions.
-template <int QT>
-__device__ __forceinline__ u32x2 to_elements(const float (&y)[8], bool odd) {
-    uint32_t w[2] = {0, 0};
-    if constexpr (QT == DT_I8) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) w[i / 4] |= ((uint32_t)(int)__builtin_rintf(y[i]) & 0xffu) << (8 * (i & 3));
-    } else if (__any(odd)) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            uint32_t b;
-            if constexpr (QT == DT_E4M3) {
-                const uint32_t u = __builtin_bit_cast(uint32_t, y[i]);
-                b = (u & 0x7fffffffu) >= 0x7f800000u ? ((u >> 24) & 0x80u) | 0x7fu : to_e4m3_sat(y[i]);
-            } else {
-                b = to_e5m2_sat(y[i]);
-            }
-            w[i / 4] |= b << (8 * (i & 3));
-        }
-    } else {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            int v = 0;
-            if constexpr (QT == DT_E4M3) {
-                v = __builtin_amdgcn_cvt_pk_fp8_f32(y[4 * h], y[4 * h + 1], v, false);
-                v = __builtin_amdgcn_cvt_pk_fp8_f32(y[4 * h + 2], y[4 * h + 3], v, true);
-            } else {
-                v = __builtin_amdgcn_cvt_pk_bf8_f32(y[4 * h], y[4 * h + 1], v, false);
-                v = __builtin_amdgcn_cvt_pk_bf8_f32(y[4 * h + 2], y[4 * h + 3], v, true);
-            }
-            w[h] = (uint32_t)v;
-        }
-    }
-    return u32x2{w[0], w[1]};
-}
 
 template <int XT, int QT>
 __global__ __launch_bounds__(256) void mx8_quantize_kernel(Mx8Params p, int64_t units, int blocks) {
@@ -88,37 +45,13 @@ __global__ __launch_bounds__(256) void mx8_quantize_kernel(Mx8Params p, int64_t 
 #pragma unroll
         for (int s = 0; s < kSteps; ++s) {
             const int64_t row = row0 + wave * kSteps + s;
-            // largest magnitude (fp32 bits order like magnitudes) over the finite elements, and whether all are
-            uint32_t m = 0, worst = 0;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const uint32_t a = __builtin_bit_cast(uint32_t, x[s][i]) & 0x7fffffffu;
-                worst = max(worst, a);
-                m = max(m, a >= 0x7f800000u ? 0u : a);
-            }
-            const auto umax = [](uint32_t a, uint32_t b) { return max(a, b); };
-            m = reduce_lanes<4>(m, umax);
-            bool odd = worst >= 0x7f800000u;
-            int e = (int)((m + (0x7fffffu - Mx8Type<QT>::frac)) >> 23) - Mx8Type<QT>::top;
-            e = m == 0 ? 127 : max(e, 1);   // at most 127 + 127 - 6 + 1
-            const float scale = __builtin_bit_cast(float, (uint32_t)(254 - e) << 23);
             float y[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] = x[s][i] * scale;
-            if constexpr (QT == DT_I8) {
-                if (reduce_lanes<4>(worst, umax) >= 0x7f800000u) {
-                    e = 255;
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) y[i] = 0.0f;
-                }
-            }
+            bool odd;
+            const int e = scale_block<QT>(x[s], y, odd);
             const u32x2 q = to_elements<QT>(y, odd);
             if (row < p.M && e0 < kp)
                 *reinterpret_cast<u32x2 *>(const_cast<uint8_t *>(p.Xq) + row * p.q_pitch + e0) = q;
-            // the word of this row: byte l16 / 4 from each group of four lanes
-            uint32_t w = (uint32_t)e << (8 * (l16 >> 2));
-            w |= dpp<kDppRor4>(w);
-            w |= dpp<kDppRor8>(w);
+            const uint32_t w = scale_word_of(e, l16);
             if (l16 == 0) words[lane >> 4][wave * kSteps + s] = w;
         }
         __syncthreads();
