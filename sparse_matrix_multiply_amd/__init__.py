@@ -627,11 +627,12 @@ def mx4_quantize(X, Xq, SX, x_type=None, stream=None):
 
 # ---- RMS norm (include/mmac_norm.h) --------------------------------------------------------------
 
-def _vector(t, n, name, dtypes=(torch.float32,)):
-    """The address of a contiguous vector of n values."""
-    if t.dtype not in dtypes:
-        raise ValueError(f"{name} has dtype {t.dtype}; expected {' or '.join(sorted(str(d) for d in dtypes))}")
-    if t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
+def _vector(t, n, name, other=torch.float32):
+    """The address of a contiguous vector of n float32 (or `other`) values."""
+    dtype = t.dtype
+    if dtype is not torch.float32 and dtype is not other:
+        raise ValueError(f"{name} has dtype {dtype}; expected {' or '.join(sorted({'torch.float32', str(other)}))}")
+    if t.shape != (n,) or (n > 1 and t.stride() != (1,)):
         raise ValueError(f"{name} must be a contiguous vector of {n} values")
     return t.data_ptr()
 
@@ -647,30 +648,30 @@ def rmsnorm(X, w, Y, eps=1e-6, residual=None, H=None, rstd=None, SY=None, stream
     float8_e4m3fn or float8_e5m2) with their scale words SY (ceil(N/128) x M int32), the operand form of gemm_mx, gemm_grouped_mx
     and gemm_mx8_wgrad.  H (h itself, may be X or residual) and rstd (r, M float32) are written when given."""
     M, N = X.shape
+    dtype = X.dtype
     tx = _input_type(X, None)
-    if Y.dtype is X.dtype:
-        ty, ldy, lds = tx, _rows_of(Y, M, N, "Y"), 0
+    lds = ldr = ldh = 0
+    at_r = at_h = at_s = None
+    if Y.dtype is dtype:
+        ty, ldy = tx, _rows_of(Y, M, N, "Y")
         if SY is not None:
             raise ValueError("SY goes with an 8-bit Y")
     elif Y.dtype is torch.float8_e4m3fn or Y.dtype is torch.float8_e5m2:
         if SY is None:
             raise ValueError("an 8-bit Y needs SY")
         ty, ldy, lds = _mx8(Y, SY, M, N, None)
+        at_s = SY.data_ptr()
     else:
-        raise ValueError(f"Y has dtype {Y.dtype}; expected {X.dtype}, float8_e4m3fn or float8_e5m2")
-    ldr = ldh = 0
+        raise ValueError(f"Y has dtype {Y.dtype}; expected {dtype}, float8_e4m3fn or float8_e5m2")
     if residual is not None:
         _same_type(residual, X, "residual")
-        ldr = _rows_of(residual, M, N, "residual")
+        ldr, at_r = _rows_of(residual, M, N, "residual"), residual.data_ptr()
     if H is not None:
         _same_type(H, X, "H")
-        ldh = _rows_of(H, M, N, "H")
-    at_w = _vector(w, N, "w", (torch.float32, X.dtype))
-    _check(lib().mmac_rmsnorm(tx, _INPUT_OF[w.dtype], ty, M, N, X.data_ptr(), _rows_of(X, M, N, "X"),
-                              residual.data_ptr() if residual is not None else None, ldr, at_w, eps,
-                              H.data_ptr() if H is not None else None, ldh, Y.data_ptr(), ldy,
-                              SY.data_ptr() if SY is not None else None, lds,
-                              _vector(rstd, M, "rstd") if rstd is not None else None,
+        ldh, at_h = _rows_of(H, M, N, "H"), H.data_ptr()
+    at_w = _vector(w, N, "w", dtype)
+    _check(lib().mmac_rmsnorm(tx, _INPUT_OF[w.dtype], ty, M, N, X.data_ptr(), _rows_of(X, M, N, "X"), at_r, ldr, at_w, eps,
+                              at_h, ldh, Y.data_ptr(), ldy, at_s, lds, _vector(rstd, M, "rstd") if rstd is not None else None,
                               _stream_of(stream, X, w, Y, residual, H, rstd, SY)), "mmac_rmsnorm")
     return Y
 
@@ -693,7 +694,7 @@ def rmsnorm_grad(dY, H, w, rstd, dX, dW=None, dH=None, workspace=None, stream=No
     for t, name in ((H, "H"), (dX, "dX"), (dH, "dH")):
         if t is not None:
             _same_type(t, dY, name)
-    at_w = _vector(w, N, "w", (torch.float32, dY.dtype))
+    at_w = _vector(w, N, "w", dY.dtype)
     ws, nbytes = _workspace_args(workspace)
     _check(lib().mmac_rmsnorm_grad(_input_type(dY, None), _INPUT_OF[w.dtype], M, N, dY.data_ptr(), _rows_of(dY, M, N, "dY"),
                                    H.data_ptr(), _rows_of(H, M, N, "H"), at_w, _vector(rstd, M, "rstd"),
@@ -725,7 +726,11 @@ def _groups_of(t, groups, rows, cols, name, wider=False):
 
 
 def _offsets(offsets, groups):
-    return _vector(offsets, groups + 1, "offsets", (torch.int32,))
+    if offsets.dtype is not torch.int32:
+        raise ValueError(f"offsets has dtype {offsets.dtype}; expected torch.int32")
+    if offsets.shape != (groups + 1,) or (groups and offsets.stride() != (1,)):
+        raise ValueError(f"offsets must be a contiguous vector of {groups + 1} values")
+    return offsets.data_ptr()
 
 
 def _group_bias(bias, groups, N):

@@ -30,15 +30,53 @@ int64_t even_tiles(int64_t groups, int64_t M, int64_t N, GroupTile t) {
     return n * ((rows + group_rows(t) - 1) / group_rows(t)) * ((N + group_cols(t) - 1) / group_cols(t));
 }
 
-GroupTile pick_tile(int64_t groups, int64_t M, int64_t N) {
-    const int64_t rows = (M + groups - 1) / groups;
-    if (rows > 128 && even_tiles(groups, M, N, GROUP_256) >= 192) return GROUP_256;
+// Tiles, measured in us (bf16, 16-bit outputs, M spread evenly; G groups of r rows, N x K weights; a tile's rows x columns).
+// Few rows, streamed weights: 16 or 32 rows x 16 columns, eight waves on K, win where tiles of 64 x 64 would leave compute
+// units idle (2 x 4096 x 4096: 16 against 32) or K is long (16 groups of 1: 113 against 121), and lose elsewhere (64 x 2 x 2048^2: 141
+// against 129).  K up to 1024 or too few tiles of 128 rows: 64 x 64 (32 x 64 x 2048 x 1024: 33 against 41).  Up to 64 rows:
+// 128 x 128 (16 x 32 x 4096^2: 130 against 157 in 64 x 64).  Beyond, the largest tile that still gives a workgroup to most
+// compute units (16 x 256 x 4096^2: 214 in 256 x 256, 230 in 128 x 128).
+GroupTile forward_tile(int64_t groups, int64_t M, int64_t N, int64_t K) {
+    const int64_t rows = (M + groups - 1) / groups, small = even_tiles(groups, M, N, GROUP_64);
+    if ((rows <= 8 && K >= 4096) || (rows <= 32 && small <= 256)) return rows <= 16 ? GROUP_16 : GROUP_32;
+    if (rows <= 16 || (rows <= 64 && K <= 1024)) return GROUP_64;
+    if (rows > 64 && even_tiles(groups, M, N, GROUP_256) >= 192) return GROUP_256;
     if (rows > 64 && even_tiles(groups, M, N, GROUP_128x256) >= 192) return GROUP_128x256;
-    if (even_tiles(groups, M, N, GROUP_128) >= 192) return GROUP_128;
+    return even_tiles(groups, M, N, GROUP_128) >= 192 ? GROUP_128 : GROUP_64;
+}
+// Weights read as K x N rows (K: the sum).  128 x 128, two workgroups a compute unit, up to 512 rows (16 x 128 x 4096^2: 184 against 208 in
+// 256 x 256; 8 x 512 x 8192 x 2048: 299 against 258), 64 x 64 for short sums or too few tiles (11 x 163, 1452 columns, K 6313: 113
+// against 142).
+GroupTile input_tile(int64_t groups, int64_t M, int64_t N, int64_t K) {
+    const int64_t rows = (M + groups - 1) / groups;
+    if (rows >= 512 && even_tiles(groups, M, N, GROUP_256) >= 192) return GROUP_256;
+    if ((rows <= 64 && K <= 1024) || even_tiles(groups, M, N, GROUP_128) < 384) return GROUP_64;
+    return GROUP_128;
+}
+// Block-scaled: a 128 x 128 tile's stages are small enough for two or three workgroups a compute unit (FP4 weights, 4 x 2048 x 4096^2:
+// 142 against 164 in 128 x 256; 16 x 64: 51 against 47; 16 x 16: 39 against 31).
+GroupTile mx_tile(int64_t groups, int64_t M, int64_t N, int64_t K) {
+    const int64_t rows = (M + groups - 1) / groups, small = even_tiles(groups, M, N, GROUP_64);
+    if ((rows <= 8 && (K > 2048 || small <= 256)) || (rows <= 32 && small <= 128)) return GROUP_16;
+    if (K <= 1152 || even_tiles(groups, M, N, GROUP_128) < 256) return GROUP_64;
+    return rows <= 128 && even_tiles(groups, M, N, GROUP_128x256) >= 192 ? GROUP_128x256 : GROUP_128;
+}
+
+// Weight gradients (us; a group's D is N x K, its sum M / groups rows long).  64 x 64, four or five workgroups a compute unit, hide
+// short sums' latencies and lose least at the edges (49 x 1109 x 1775 bf16 from 20 rows each: 178, in 256 x 256 237; 7 x 1965 x 1924
+// fp32 from 4: 42 against 63).  256 x 256 for long sums (4 x 4096^2 from 2048 rows: 290 against 441) and, where they fill their tiles, for
+// many large matrices in 16 bits (16 x 4096^2 from 32 rows: 204 against 241); those in fp32, whose C and D take the time, in 128 x 128 (440,
+// 473 in 256 x 256).
+GroupTile wgrad_tile(int64_t groups, int64_t M, int64_t N, int64_t K, int64_t tiles, bool fp32) {
+    const int64_t rows = M / groups;
+    const double filled = (double)groups * N * K / (65536.0 * tiles);   // share of the 256 x 256 tiles that is D
+    if (rows >= 512 && tiles >= 192 && filled >= 0.8) return GROUP_256;
+    if (tiles >= 1024 && filled >= 0.91) return fp32 ? GROUP_128 : GROUP_256;
     return GROUP_64;
 }
 
-// The most tiles that M rows in `groups` groups can make: n groups with rows, all but one row of each spread evenly.
+// The most tiles that M rows in `groups` groups can make: n groups with rows, all but one row of each spread evenly
+// (a half tile counts as one).
 int64_t most_tiles(int64_t groups, int64_t M, int rows, int64_t columns) {
     const int64_t n = std::min(groups, M);
     return (n + (M - n) / rows) * columns;
@@ -96,7 +134,7 @@ GemmParams make_params(int64_t M, int64_t N, int64_t K, double alpha, const void
 // Tile counts of the forward products and their grid; false if it would pass a 32-bit count of threads.
 bool set_grid(GemmParams &p, int64_t groups, int rows, int cols, int64_t &grid) {
     const int64_t tn = (p.N + cols - 1) / cols;
-    grid = (most_tiles(groups, p.M, rows, tn) + 7) / 8 * 8;
+    grid = (most_tiles(groups, p.M, rows, tn) + 7) / 8 * 8 + 8;   // either kind of tile may leave some XCDs one short
     if (tn > INT32_MAX / 1024 || grid > INT32_MAX / 1024) return false;
     p.tiles_n = (int)tn;
     p.tiles_m = 0;   // differs by group
@@ -129,9 +167,8 @@ mmac_status_t mmac_gemm_grouped(mmac_dtype_t a_type, int trans_b, int64_t groups
     if (trans_b && K * ldb * 2 >= ((int64_t)1 << 31)) return MMAC_ERR_UNSUPPORTED;
     if (empty) return MMAC_OK;
 
-    const int64_t rows = (M + groups - 1) / groups;
     const int forced = forced_tile();
-    GroupTile t = forced >= 0 ? (GroupTile)forced : !trans_b && rows <= 16 ? GROUP_16 : !trans_b && rows <= 32 ? GROUP_32 : pick_tile(groups, M, N);
+    GroupTile t = forced >= 0 ? (GroupTile)forced : trans_b ? input_tile(groups, M, N, K) : forward_tile(groups, M, N, K);
     if (trans_b && (t == GROUP_16 || t == GROUP_32)) t = GROUP_64;
     GemmParams p = make_params(M, N, K, alpha, A, lda * 2, B, ldb * 2, beta, C, ldc, D, ldd, ep);
     Groups g{};
@@ -174,9 +211,8 @@ mmac_status_t mmac_gemm_grouped_mx(mmac_dtype_t a_type, mmac_dtype_t b_type, int
     if (st != MMAC_OK) return st;
     if (empty) return MMAC_OK;
 
-    const int64_t rows = (M + groups - 1) / groups;
     const int forced = forced_tile();
-    GroupTile t = forced >= 0 ? (GroupTile)forced : rows <= 16 ? GROUP_16 : pick_tile(groups, M, N);
+    GroupTile t = forced >= 0 ? (GroupTile)forced : mx_tile(groups, M, N, K);
     if (t == GROUP_32) t = GROUP_16;
     if (t == GROUP_256) t = GROUP_128x256;   // the 256 x 256 tile has no registers left for the scale words
     GemmParams p = make_params(M, N, K, alpha, A, lda, B, ldb / per, beta, C, ldc, D, ldd, ep);
@@ -221,14 +257,9 @@ mmac_status_t mmac_gemm_grouped_wgrad(mmac_dtype_t y_type, int64_t groups, int64
 
     const auto tiles = [&](GroupTile t) { return groups * ((N + group_rows(t) - 1) / group_rows(t)) * ((K + group_cols(t) - 1) / group_cols(t)); };
     const int forced = forced_tile();
-    GroupTile t = forced >= 0                       ? (GroupTile)forced
-                  : tiles(GROUP_256) >= 192         ? GROUP_256
-                  : tiles(GROUP_128x256) >= 192     ? GROUP_128x256
-                  : tiles(GROUP_128) >= 192         ? GROUP_128
-                                                    : GROUP_64;
+    GroupTile t = forced >= 0 ? (GroupTile)forced : wgrad_tile(groups, M, N, K, tiles(GROUP_256), ep.d_type == MMAC_OUT_ACC);
     if (t == GROUP_16 || t == GROUP_32) t = GROUP_64;
-    const int64_t grid = tiles(t);
-    if (grid > INT32_MAX / 1024) return MMAC_ERR_UNSUPPORTED;
+    if (tiles(t) > INT32_MAX / 1024 / 8) return MMAC_ERR_UNSUPPORTED;   // the grid, with up to 7 idle workgroups a group
     GemmParams p = make_params(N, K, 0, alpha, dY, ldy * 2, X, ldx * 2, beta, C, ldc, D, ldd, ep);
     p.tiles_m = (int)((N + group_rows(t) - 1) / group_rows(t));
     p.tiles_n = (int)((K + group_cols(t) - 1) / group_cols(t));
@@ -243,7 +274,7 @@ mmac_status_t mmac_gemm_grouped_wgrad(mmac_dtype_t y_type, int64_t groups, int64
     p.vec_d = p.vec_d && g.d_stride % 16 == 0;
     p.vec_c = p.vec_c && g.c_stride % 16 == 0;
     g.span = (int)((((int64_t)1 << 31) - 1) / (std::max(ldy, ldx) * 2) / 64 * 64);   // at least 192: pitches are at most 8 MiB
-    return launched(launch_gemm_grouped_wgrad(y_type, t, p, g, grid, static_cast<hipStream_t>(stream)));
+    return launched(launch_gemm_grouped_wgrad(y_type, t, p, g, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -150,6 +150,32 @@ __device__ __forceinline__ float from_out_bits(uint32_t h) {
     }
 }
 
+// N values to bf16 or binary16 with the same rules, two a word.  The conversion instructions round to nearest even and
+// keep subnormals; only where a lane of the wave holds a value that is not finite or would round past the largest do the bit-level
+// forms above decide (one comparison an element instead of about ten instructions).
+template <int OT, int N>
+__device__ __forceinline__ void pack16_sat(const float (&v)[N], uint32_t (&o)[N / 2]) {
+    static_assert(OT == OUT_BF16 || OT == OUT_F16, "16-bit types");
+    typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+    typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
+    const float past = __builtin_bit_cast(float, OT == OUT_BF16 ? 0x7f7f8000u : 0x477ff000u);   // the first magnitude that rounds past it
+    bool odd = false;
+#pragma unroll
+    for (int i = 0; i < N; ++i) odd |= !(__builtin_fabsf(v[i]) < past);
+    if (__builtin_expect(__any(odd), 0)) {
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i)
+            o[i] = OT == OUT_BF16 ? to_bf16_sat(v[2 * i]) | (to_bf16_sat(v[2 * i + 1]) << 16)
+                                  : to_f16_sat(v[2 * i]) | (to_f16_sat(v[2 * i + 1]) << 16);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) {
+            if constexpr (OT == OUT_BF16) o[i] = __builtin_bit_cast(uint32_t, bf16x2_t{(__bf16)v[2 * i], (__bf16)v[2 * i + 1]});
+            else o[i] = __builtin_bit_cast(uint32_t, f16x2_t{(_Float16)v[2 * i], (_Float16)v[2 * i + 1]});
+        }
+    }
+}
+
 // The end of every floating epilogue: v = alpha * acc + beta * C already
 // formed in fp32; add the column's bias (when there is one), apply ReLU (when
 // asked: negative values become +0, NaN and -0 pass), and round to D's type.

@@ -8,7 +8,7 @@ namespace mmac {
 template <class Op>
 hipError_t launch_grouped_op(GroupTile t, const GemmParams &p, const Groups &g, int64_t blocks, hipStream_t s);
 template <class Op>
-hipError_t launch_grouped_wgrad_op(GroupTile t, const GemmParams &p, const Groups &g, int64_t blocks, hipStream_t s);
+hipError_t launch_grouped_wgrad_op(GroupTile t, const GemmParams &p, const Groups &g, hipStream_t s);
 // grouped_rows.hip, grouped_mx_rows.hip
 hipError_t launch_gemm_grouped_rows(int dt, GroupTile t, const GemmParams &p, const Groups &g, int64_t blocks, hipStream_t s);
 hipError_t launch_gemm_grouped_mx_rows(int a, int b, const GemmParams &p, const Groups &g, int64_t blocks, hipStream_t s);
@@ -24,9 +24,9 @@ hipError_t launch_gemm_grouped(int dt, bool trans_b, GroupTile t, GemmParams p, 
     return hipErrorInvalidValue;
 }
 
-hipError_t launch_gemm_grouped_wgrad(int dt, GroupTile t, GemmParams p, Groups g, int64_t blocks, hipStream_t s) {
-    if (dt == DT_BF16) return launch_grouped_wgrad_op<Trans<MmaDense16<DT_BF16>, true, true>>(t, p, g, blocks, s);
-    if (dt == DT_F16) return launch_grouped_wgrad_op<Trans<MmaDense16<DT_F16>, true, true>>(t, p, g, blocks, s);
+hipError_t launch_gemm_grouped_wgrad(int dt, GroupTile t, GemmParams p, Groups g, hipStream_t s) {
+    if (dt == DT_BF16) return launch_grouped_wgrad_op<Trans<MmaDense16<DT_BF16>, true, true>>(t, p, g, s);
+    if (dt == DT_F16) return launch_grouped_wgrad_op<Trans<MmaDense16<DT_F16>, true, true>>(t, p, g, s);
     return hipErrorInvalidValue;
 }
 

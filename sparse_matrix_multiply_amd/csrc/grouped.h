@@ -30,25 +30,40 @@ inline int group_cols(GroupTile t) {
 constexpr int kMxRowsCols = 32;
 
 hipError_t launch_gemm_grouped(int dt, bool trans_b, GroupTile t, GemmParams p, Groups g, int64_t grid, hipStream_t s);
-hipError_t launch_gemm_grouped_wgrad(int dt, GroupTile t, GemmParams p, Groups g, int64_t grid, hipStream_t s);
+hipError_t launch_gemm_grouped_wgrad(int dt, GroupTile t, GemmParams p, Groups g, hipStream_t s);
 hipError_t launch_gemm_grouped_mx(int dt_a, int dt_b, GroupTile t, GemmParams p, Groups g, int64_t grid, hipStream_t s);
 
 #if defined(__HIPCC__)
 
-// A workgroup's tile: rows first .. first + rows - 1 of the arrays are group g's, (tm, tn) the tile within them.
+// A workgroup's tile: rows first .. first + rows - 1 of the arrays are group g's; the tile begins at row `top` of them, in
+// column tile tn.  low: the tile is one of BM / 2 rows.
 struct GroupTileAt {
-    int g, first, rows, tm, tn;
+    int g, first, rows, top, tn;
+    bool low;
 };
 
+// Sum over the lanes up to and with this one.
+__device__ __forceinline__ int lanes_up_to(int v) {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+        const int x = __shfl_up(v, d);
+        v += lane >= d ? x : 0;
+    }
+    return v;
+}
+
 // Workgroup -> (group, tile), from the offsets alone.  Every wave looks for itself, 64 groups at a time: lane i has group
-// base + i, its number of tile rows, and the sum of those before it.  The tiles are numbered group by group,
-// within a group as tile_coords numbers them, and dealt to the XCDs in contiguous runs, so tiles that share a
-// group's weights are in one L2.  Returns false for the workgroups behind the last tile: the host only
-// knows the most tiles there can be.  A range that leaves the arrays is cut to them, a decreasing one is empty.
-template <int BM>
+// base + i, its number of tile rows, and the sum of those before it.  Tiles are BM rows high; with HALF, what is left of a group
+// after them takes a tile of BM / 2 rows when it fits one, and all of those come last, so that the compute units that are free
+// first at the end find short work.  Either kind is numbered group by group, within a group in bands of group_m tile rows,
+// column by column, and dealt to the XCDs in contiguous runs, so tiles that share a group's weights are in one
+// L2.  Returns false for the workgroups behind the last tile: the host only knows the most tiles there can
+// be.  A range that leaves the arrays is cut to them, a decreasing one is empty.
+template <int BM, bool HALF>
 __device__ __forceinline__ bool find_group_tile(const Groups &q, int tiles_n, int group_m, int wg, GroupTileAt &at) {
     const int lane = threadIdx.x & 63;
-    const auto tiles_of = [&](int g, int &first, int &rows) {
+    const auto rows_of = [&](int g, int &first, int &rows) {
         first = 0;
         int end = 0;
         if (g < q.count) {
@@ -56,26 +71,30 @@ __device__ __forceinline__ bool find_group_tile(const Groups &q, int tiles_n, in
             end = min(max(q.offsets[g + 1], first), q.rows);
         }
         rows = end - first;
-        return (rows + BM - 1) / BM;
     };
-    const auto up_to = [&](int v) {   // inclusive sum over the lanes
-#pragma unroll
-        for (int d = 1; d < 64; d *= 2) {
-            const int x = __shfl_up(v, d);
-            v += lane >= d ? x : 0;
-        }
-        return v;
-    };
-    int first, rows, sum = 0;
-    const int own0 = up_to(tiles_of(lane, first, rows));
-    int total = __builtin_amdgcn_readlane(own0, 63);
-    const int first0 = first, rows0 = rows;
-    for (int base = 64; base < q.count; base += 64) total += __builtin_amdgcn_readlane(up_to(tiles_of(base + lane, first, rows)), 63);
-
-    const int U = total * tiles_n, x = wg & 7, local = wg >> 3, per = U >> 3, more = U & 7;
-    if (local >= per + (x < more ? 1 : 0)) return false;
-    const int u = x * per + min(x, more) + local, row_tile = u / tiles_n;
-    int up = own0, base = 0;
+    const auto whole = [](int rows) { return HALF ? (rows + BM / 2 - 1) / BM : (rows + BM - 1) / BM; };
+    const auto half = [](int rows) { return HALF && rows % BM > 0 && rows % BM <= BM / 2 ? 1 : 0; };
+    int first, rows;
+    rows_of(lane, first, rows);
+    const int first0 = first, rows0 = rows, up0 = lanes_up_to(whole(rows)), low0 = HALF ? lanes_up_to(half(rows)) : 0;
+    int total = __builtin_amdgcn_readlane(up0, 63), total_low = HALF ? __builtin_amdgcn_readlane(low0, 63) : 0;
+    for (int base = 64; base < q.count; base += 64) {
+        rows_of(base + lane, first, rows);
+        total += __builtin_amdgcn_readlane(lanes_up_to(whole(rows)), 63);
+        if (HALF) total_low += __builtin_amdgcn_readlane(lanes_up_to(half(rows)), 63);
+    }
+    const int x = wg & 7;
+    int local = wg >> 3, U = total * tiles_n, mine = (U >> 3) + (x < (U & 7) ? 1 : 0);
+    at.low = false;
+    if (HALF && local >= mine) {
+        local -= mine;
+        U = total_low * tiles_n;
+        mine = (U >> 3) + (x < (U & 7) ? 1 : 0);
+        at.low = true;
+    }
+    if (local >= mine) return false;
+    const int u = x * (U >> 3) + min(x, U & 7) + local, row_tile = u / tiles_n;
+    int up = at.low ? low0 : up0, base = 0, sum = 0;
     first = first0;
     rows = rows0;
     for (;;) {
@@ -85,30 +104,33 @@ __device__ __forceinline__ bool find_group_tile(const Groups &q, int tiles_n, in
             at.g = base + l;
             at.first = __builtin_amdgcn_readlane(first, l);
             at.rows = __builtin_amdgcn_readlane(rows, l);
-            const int mine = (at.rows + BM - 1) / BM;
-            const int in = u - (sum + __builtin_amdgcn_readlane(up, l) - mine) * tiles_n;
-            const int per_band = group_m * tiles_n, band = in / per_band, top = band * group_m;
-            const int high = min(mine - top, group_m), rest = in - band * per_band;
-            at.tm = top + rest % high;
-            at.tn = rest / high;
+            const int count = at.low ? 1 : whole(at.rows);
+            const int in = u - (sum + __builtin_amdgcn_readlane(up, l) - count) * tiles_n;
+            const int per_band = group_m * tiles_n, band = in / per_band, above = band * group_m;
+            const int high = min(count - above, group_m), rest = in - band * per_band;
+            at.top = __builtin_amdgcn_readfirstlane(at.low ? at.rows / BM * BM : (above + rest % high) * BM);
+            at.tn = __builtin_amdgcn_readfirstlane(rest / high);
+            at.g = __builtin_amdgcn_readfirstlane(at.g);
             return true;
         }
         sum += __builtin_amdgcn_readlane(up, 63);
         base += 64;
         if (base >= q.count) return false;   // not reached: row_tile is below the total
-        up = up_to(tiles_of(base + lane, first, rows));
+        rows_of(base + lane, first, rows);
+        up = lanes_up_to(at.low ? half(rows) : whole(rows));
     }
 }
 
-// The group's part of the arrays (forward and input gradient).
-__device__ __forceinline__ void take_group(GemmParams &p, const Groups &q, const GroupTileAt &at) {
+// The group's part of the arrays (forward and input gradient), from row `from` of its rows on.
+__device__ __forceinline__ void take_group(GemmParams &p, const Groups &q, const GroupTileAt &at, int from) {
     const int es = p.d_type == 0 ? 4 : p.d_type <= 2 ? 2 : 1;
-    p.A += (int64_t)at.first * p.a_pitch;
+    const int64_t row = at.first + from;
+    p.A += row * p.a_pitch;
     p.B += at.g * q.b_stride;
-    p.D = static_cast<uint8_t *>(p.D) + (int64_t)at.first * p.ldd * es;
-    if (p.use_c) p.C = static_cast<const uint8_t *>(p.C) + (int64_t)at.first * p.ldc * es;
+    p.D = static_cast<uint8_t *>(p.D) + row * p.ldd * es;
+    if (p.use_c) p.C = static_cast<const uint8_t *>(p.C) + row * p.ldc * es;
     if (p.bias) p.bias += at.g * q.bias_stride;
-    p.M = at.rows;
+    p.M = at.rows - from;
 }
 
 #endif  // __HIPCC__

@@ -6,31 +6,50 @@
 
 namespace mmac {
 
-template <class Op, int BM, int BN, int WM, int WN, int STAGES>
-__global__ __launch_bounds__(WM *WN * 64) __attribute__((amdgpu_waves_per_eu(WM * WN / 4, WM * WN / 4)))
-void gemm_grouped_kernel(GemmParams p, Groups q) {
-    typedef TiledGemm<Op, BM, BN, WM, WN, STAGES> T;
-    __shared__ __attribute__((aligned(16))) uint8_t smem[T::LDS_BYTES];
-    GroupTileAt at;
-    if (!find_group_tile<BM>(q, p.tiles_n, p.group_m, blockIdx.x, at)) return;
-    take_group(p, q, at);
-    if constexpr (T::SCALED) p.sb += at.g * q.sb_stride;
-    T t(p, at.tm, at.tn, 0, at.first);
+template <class T, class Op, int BM>
+__device__ __forceinline__ void group_tile(const GemmParams &p, const GroupTileAt &at, uint8_t *smem) {
+    T t(p, at.top / BM, at.tn, 0, at.first);
     if constexpr (T::SPARE_BYTES > 0) t.spare = smem + T::STAGES * T::STAGE + t.wave * 256;
     walk_k<T, Op>(t, smem);
     t.epilogue(smem);
 }
 
+// One workgroup per tile of BM x BN, WM x WN waves; HALF: or of BM / 2 x BN, for the last rows of a group.
+template <class Op, int BM, int BN, int WM, int WN, int STAGES, bool HALF, int PER_CU = 1>
+__global__ __launch_bounds__(WM *WN * 64) __attribute__((amdgpu_waves_per_eu(WM * WN * PER_CU / 4, WM * WN * PER_CU / 4)))
+void gemm_grouped_kernel(GemmParams p, Groups q) {
+    typedef TiledGemm<Op, BM, BN, WM, WN, STAGES> T;
+    typedef TiledGemm<Op, HALF ? BM / 2 : BM, BN, WM, WN, HALF ? 3 : STAGES> L;
+    __shared__ __attribute__((aligned(16))) uint8_t smem[T::LDS_BYTES > L::LDS_BYTES ? T::LDS_BYTES : L::LDS_BYTES];
+    GroupTileAt at;
+    if (!find_group_tile<BM, HALF>(q, p.tiles_n, p.group_m, blockIdx.x, at)) return;
+    take_group(p, q, at, 0);
+    if constexpr (T::SCALED) p.sb += at.g * q.sb_stride;
+    if constexpr (HALF)
+        if (at.low) return group_tile<L, Op, BM / 2>(p, at, smem);
+    group_tile<T, Op, BM>(p, at, smem);
+}
+
 // Weight gradient: the tiles of every group's D, the sum over the group's rows (both operands' K is strided).  A sum
 // over more rows than one buffer descriptor covers is walked in parts, each with descriptors of its own.
-template <class Op, int BM, int BN, int WM, int WN, int STAGES>
-__global__ __launch_bounds__(WM *WN * 64) __attribute__((amdgpu_waves_per_eu(WM * WN / 4, WM * WN / 4)))
+template <class Op, int BM, int BN, int WM, int WN, int STAGES, int PER_CU = 1>
+__global__ __launch_bounds__(WM *WN * 64) __attribute__((amdgpu_waves_per_eu(WM * WN * PER_CU / 4, WM * WN * PER_CU / 4)))
 void gemm_grouped_wgrad_kernel(GemmParams p, Groups q) {
     typedef TiledGemm<Op, BM, BN, WM, WN, STAGES> T;
     __shared__ __attribute__((aligned(16))) uint8_t smem[T::LDS_BYTES];
-    // contiguous runs of tiles per XCD, as in tile_coords, the groups one after the other
-    const int per = p.tiles_m * p.tiles_n, U = per * q.count, x = blockIdx.x & 7;
-    const int u = x * (U >> 3) + min(x, U & 7) + (int)(blockIdx.x >> 3), g = u / per, in = u - g * per;
+    // The groups one after the other; a group's tiles in contiguous runs per XCD where there are some for each, so that a long
+    // group is every XCD's.
+    const int per = p.tiles_m * p.tiles_n, x = blockIdx.x & 7, share = (per + 7) / 8;
+    int g, in;
+    if (per >= 64) {
+        const int local = blockIdx.x >> 3, mine = local % share;
+        g = local / share;
+        if (mine >= (per >> 3) + (x < (per & 7) ? 1 : 0)) return;
+        in = x * (per >> 3) + min(x, per & 7) + mine;
+    } else {
+        g = blockIdx.x / per;
+        in = blockIdx.x - g * per;
+    }
     const int band = in / (p.group_m * p.tiles_n), top = band * p.group_m, high = min(p.tiles_m - top, p.group_m);
     const int rest = in - band * p.group_m * p.tiles_n;
     const int first = __builtin_amdgcn_readfirstlane(min(max(q.offsets[g], 0), q.rows));
@@ -57,13 +76,17 @@ void gemm_grouped_wgrad_kernel(GemmParams p, Groups q) {
 template <class Op>
 hipError_t launch_grouped_op(GroupTile tile, const GemmParams &p, const Groups &g, int64_t blocks, hipStream_t s) {
     const dim3 grid((unsigned)blocks);
+    // workgroups of the small tiles that fit a compute unit's 160 KiB of LDS
+    constexpr int L64 = TiledGemm<Op, 64, 64, 2, 2, 2>::LDS_BYTES, L128 = TiledGemm<Op, 128, 128, 2, 2, 2>::LDS_BYTES;
+    constexpr int P64 = 160 * 1024 / L64 < 4 ? 160 * 1024 / L64 : 4, P128 = 160 * 1024 / L128 < 3 ? 160 * 1024 / L128 : 3;
     switch (tile) {
-    case GROUP_64: hipLaunchKernelGGL((gemm_grouped_kernel<Op, 64, 64, 2, 2, 4>), grid, dim3(256), 0, s, p, g); break;
-    case GROUP_128: hipLaunchKernelGGL((gemm_grouped_kernel<Op, 128, 128, 2, 2, 4>), grid, dim3(256), 0, s, p, g); break;
-    case GROUP_128x256: hipLaunchKernelGGL((gemm_grouped_kernel<Op, 128, 256, 2, 4, 3>), grid, dim3(512), 0, s, p, g); break;
+    case GROUP_64: hipLaunchKernelGGL((gemm_grouped_kernel<Op, 64, 64, 2, 2, 2, false, P64>), grid, dim3(256), 0, s, p, g); break;
+    case GROUP_128: hipLaunchKernelGGL((gemm_grouped_kernel<Op, 128, 128, 2, 2, 2, false, P128>), grid, dim3(256), 0, s, p, g); break;
+    // block-scaled products take this tile for groups of up to 128 rows: a half tile would change little
+    case GROUP_128x256: hipLaunchKernelGGL((gemm_grouped_kernel<Op, 128, 256, 2, 4, 3, !Op::kScaled>), grid, dim3(512), 0, s, p, g); break;
     case GROUP_256:
         if constexpr (Op::kScaled) return hipErrorInvalidValue;   // no registers left for the scale words
-        else hipLaunchKernelGGL((gemm_grouped_kernel<Op, 256, 256, 2, 4, 2>), grid, dim3(512), 0, s, p, g);
+        else hipLaunchKernelGGL((gemm_grouped_kernel<Op, 256, 256, 2, 4, 2, true>), grid, dim3(512), 0, s, p, g);
         break;
     default: return hipErrorInvalidValue;
     }
@@ -71,11 +94,12 @@ hipError_t launch_grouped_op(GroupTile tile, const GemmParams &p, const Groups &
 }
 
 template <class Op>
-hipError_t launch_grouped_wgrad_op(GroupTile tile, const GemmParams &p, const Groups &g, int64_t blocks, hipStream_t s) {
-    const dim3 grid((unsigned)blocks);
+hipError_t launch_grouped_wgrad_op(GroupTile tile, const GemmParams &p, const Groups &g, hipStream_t s) {
+    const int64_t per = (int64_t)p.tiles_m * p.tiles_n;
+    const dim3 grid((unsigned)(per >= 64 ? (per + 7) / 8 * 8 * g.count : per * g.count));   // as the kernel counts
     switch (tile) {
-    case GROUP_64: hipLaunchKernelGGL((gemm_grouped_wgrad_kernel<Op, 64, 64, 2, 2, 4>), grid, dim3(256), 0, s, p, g); break;
-    case GROUP_128: hipLaunchKernelGGL((gemm_grouped_wgrad_kernel<Op, 128, 128, 2, 2, 4>), grid, dim3(256), 0, s, p, g); break;
+    case GROUP_64: hipLaunchKernelGGL((gemm_grouped_wgrad_kernel<Op, 64, 64, 2, 2, 2, 5>), grid, dim3(256), 0, s, p, g); break;
+    case GROUP_128: hipLaunchKernelGGL((gemm_grouped_wgrad_kernel<Op, 128, 128, 2, 2, 2, 2>), grid, dim3(256), 0, s, p, g); break;
     case GROUP_128x256: hipLaunchKernelGGL((gemm_grouped_wgrad_kernel<Op, 128, 256, 2, 4, 3>), grid, dim3(512), 0, s, p, g); break;
     case GROUP_256: hipLaunchKernelGGL((gemm_grouped_wgrad_kernel<Op, 256, 256, 2, 4, 2>), grid, dim3(512), 0, s, p, g); break;
     default: return hipErrorInvalidValue;

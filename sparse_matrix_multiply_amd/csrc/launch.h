@@ -45,8 +45,8 @@ struct GemmParams {
     // 16 bytes, so the epilogue may store 16 consecutive bytes of a row with
     // one access.
     int vec_d;
-    // vec_c: the same for C (16- and 8-bit C is read four elements at a time
-    // when it holds).
+    // vec_c: the same for C (the wide accesses are buffer accesses when it holds,
+    // unaligned global ones otherwise).
     int vec_c;
     // Epilogue variant (floating inputs only): d_type is OUT_ACC (C and D are
     // fp32) or one of the 16- / 8-bit types (C and D are of that type; C is

@@ -1,7 +1,7 @@
 // RMS norm, forward: h = x + residual, y = h * rstd * w with rstd = (mean(h^2) + eps)^(-1/2), in one pass over memory.
 //
 // A row of N elements is held in registers by T threads with V groups of eight elements each (T = 64: one wave per
-// row, four rows a workgroup; 256 and 1024: a workgroup per row), so x and the residual are read once, h and y
+// row, four rows a workgroup; 256 to 1024: a workgroup per row), so x and the residual are read once, h and y
 // written once.  Rows longer than 32768 are walked twice, the second time from the caches.
 // Sums, rstd and the products of y are fp32.
 #include <algorithm>
@@ -49,19 +49,21 @@ struct NormOut {
 };
 
 template <int WT>
-__device__ __forceinline__ void load_weight(float (&w)[8], const void *at, int e0, int N) {
+__device__ __forceinline__ Raw8<WT> load_weight(const void *at, int e0, int N) {
     const RowOf<WT> r(at, 0, 0, N);
     Raw8<WT> x = load_raw8<WT, 0>(r.whole, e0);
     if (N & 7)
         if (e0 == (N & ~7)) r.load_short(x, e0, N & 7);
-    elements<WT>(x, w);
+    return x;
 }
 
 // h's eight elements at e0 from x's and the residual's, as they are kept: rounded to X's type.
 template <int XT>
 __device__ __forceinline__ void add_residual(float (&h)[8], const Raw8<XT> &x, const Raw8<XT> &r) {
+    float sum[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) h[i] = from_bits<XT>(rounded<XT>(element<XT>(x, i) + element<XT>(r, i)));
+    for (int i = 0; i < 8; ++i) sum[i] = element<XT>(x, i) + element<XT>(r, i);
+    elements<XT>(pack8<XT>(sum), h);
 }
 
 template <int XT, int WT, int OT, int T, int V>
@@ -71,6 +73,13 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void rmsnorm_kernel(NormParams p
     const int t = threadIdx.x % T, sub = __builtin_amdgcn_readfirstlane(threadIdx.x / T);
     const int N = p.N;
     const XcdPart part(units);
+    // the weight too stays in registers, from before the first row on, where they suffice
+    constexpr bool KEEP = V <= 2;
+    Raw8<WT> wr[V];
+    if constexpr (KEEP) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) wr[v] = load_weight<WT>(p.w, (v * T + t) * 8, N);
+    }
     int turn = 0;
     for (int64_t u = blockIdx.x >> 3; u < part.count; u += gridDim.x >> 3) {
         const int64_t row = (part.first + u) * ROWS + sub;
@@ -118,7 +127,8 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void rmsnorm_kernel(NormParams p
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             float w[8];
-            load_weight<WT>(w, p.w, (v * T + t) * 8, N);
+            if constexpr (KEEP) elements<WT>(wr[v], w);
+            else elements<WT>(load_weight<WT>(p.w, (v * T + t) * 8, N), w);
             out.put(h[v], w, rstd, (v * T + t) * 8);
         }
     }
@@ -176,7 +186,7 @@ __global__ __launch_bounds__(1024) void rmsnorm_long_kernel(NormParams p, int64_
             } else {
                 form(h, e0);
             }
-            load_weight<WT>(w, p.w, e0, N);
+            elements<WT>(load_weight<WT>(p.w, e0, N), w);
             out.put(h, w, rstd, e0);
         }
     }
@@ -191,7 +201,7 @@ static hipError_t launch_as(const NormParams &p, hipStream_t s) {
     else if (p.N <= 1024) hipLaunchKernelGGL((rmsnorm_kernel<XT, WT, OT, 64, 2>), grid(four), dim3(256), 0, s, p, four);
     else if (p.N <= 2048) hipLaunchKernelGGL((rmsnorm_kernel<XT, WT, OT, 256, 1>), grid(p.M), dim3(256), 0, s, p, p.M);
     else if (p.N <= 4096) hipLaunchKernelGGL((rmsnorm_kernel<XT, WT, OT, 256, 2>), grid(p.M), dim3(256), 0, s, p, p.M);
-    else if (p.N <= 8192) hipLaunchKernelGGL((rmsnorm_kernel<XT, WT, OT, 256, 4>), grid(p.M), dim3(256), 0, s, p, p.M);
+    else if (p.N <= 8192) hipLaunchKernelGGL((rmsnorm_kernel<XT, WT, OT, 512, 2>), grid(p.M), dim3(512), 0, s, p, p.M);
     else if (p.N <= 16384) hipLaunchKernelGGL((rmsnorm_kernel<XT, WT, OT, 1024, 2>), grid(p.M), dim3(1024), 0, s, p, p.M);
     else if (p.N <= 32768) hipLaunchKernelGGL((rmsnorm_kernel<XT, WT, OT, 1024, 4>), grid(p.M), dim3(1024), 0, s, p, p.M);
     else hipLaunchKernelGGL((rmsnorm_long_kernel<XT, WT, OT>), grid(p.M), dim3(1024), 0, s, p, p.M);

@@ -54,8 +54,10 @@ __device__ __forceinline__ Raw8<DT> pack8(const float (&f)[8]) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) x.d[i / 4][i % 4] = (int)rounded<DT>(f[i]);
     } else {
+        uint32_t o[4];
+        pack16_sat<DT == DT_BF16 ? OUT_BF16 : OUT_F16>(f, o);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x.d[0][i] = (int)(rounded<DT>(f[2 * i]) | (rounded<DT>(f[2 * i + 1]) << 16));
+        for (int i = 0; i < 4; ++i) x.d[0][i] = (int)o[i];
     }
     return x;
 }
