@@ -51,8 +51,11 @@ mmac_status_t mmac_gemm_grouped(mmac_dtype_t a_type, int trans_b, int64_t groups
  *             are at SB + g * stride_sb, ceil(K/128) x ldsb, ldsb >= N, 4-byte aligned.
  *             Each array (a group's, for B) spans less than 2^31 bytes.
  *   lda, ldb, stride_b count elements (FP4: two per byte; rows start on 16 bytes).
- * e = 255 in a block that is used gives unspecified results.  The rest as in
- * mmac_gemm_grouped.
+ * e = 255 in a block that is used gives unspecified results.
+ * Sums are fp32.  Outputs of 16 and 8 bits come from the block-scaled matrix instructions,
+ * whose own error (up to 2^-13 of the sum of magnitudes) is below what such an output
+ * rounds; for fp32 outputs the elements times their scales become bf16, exact for magnitudes
+ * from 2^-126 to bf16's largest, and their products are exact.  The rest as in mmac_gemm_grouped.
  */
 mmac_status_t mmac_gemm_grouped_mx(mmac_dtype_t a_type, mmac_dtype_t b_type, int64_t groups, int64_t M, int64_t N,
                                    int64_t K, double alpha, const void *A, int64_t lda, const uint32_t *SA,

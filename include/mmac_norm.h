@@ -52,7 +52,7 @@ mmac_status_t mmac_rmsnorm(mmac_dtype_t x_type, mmac_dtype_t w_type, mmac_dtype_
  *   dH        NULL (lddh unused) or the gradient that reaches h on the residual stream.
  *   dW        NULL, or N fp32 values, 16-byte aligned.
  *   workspace device memory, 16-byte aligned, for the partial sums of dW: at least
- *             mmac_rmsnorm_grad_workspace_bytes (MMAC_ERR_SCRATCH otherwise); unused
+ *             mmac_rmsnorm_grad_workspace_bytes (MMAC_ERR_INVALID_ARG otherwise); unused
  *             without dW.  It need not be cleared, and its first KiB is left alone, so
  *             it may be a workspace that the products share, in one stream.
  * dX may be dY or dH (with the same pitch).  The sums are added up in a fixed order:

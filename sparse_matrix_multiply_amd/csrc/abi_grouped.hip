@@ -34,13 +34,13 @@ int64_t even_tiles(int64_t groups, int64_t M, int64_t N, GroupTile t) {
 // Few rows, streamed weights: 16 or 32 rows x 16 columns, eight waves on K, win where tiles of 64 x 64 would leave compute
 // units idle (2 x 4096 x 4096: 16 against 32) or K is long (16 groups of 1: 113 against 121), and lose elsewhere (64 x 2 x 2048^2: 141
 // against 129).  K up to 1024 or too few tiles of 128 rows: 64 x 64 (32 x 64 x 2048 x 1024: 33 against 41).  Up to 64 rows:
-// 128 x 128 (16 x 32 x 4096^2: 130 against 157 in 64 x 64).  Beyond, the largest tile that still gives a workgroup to most
-// compute units (16 x 256 x 4096^2: 214 in 256 x 256, 230 in 128 x 128).
+// 128 x 128 (16 x 32 x 4096^2: 130 against 157 in 64 x 64).  Up to 384 rows: 128 x 256 (16 x 256 x 4096^2: 213, in 256 x 256
+// 226); beyond, 256 x 256 (16 x 512 x 4096^2: 331, in 128 x 256 339; 8 x 1024 x 1024 x 2048, 128 tiles: 55, 62), where there are enough.
 GroupTile forward_tile(int64_t groups, int64_t M, int64_t N, int64_t K) {
     const int64_t rows = (M + groups - 1) / groups, small = even_tiles(groups, M, N, GROUP_64);
     if ((rows <= 8 && K >= 4096) || (rows <= 32 && small <= 256)) return rows <= 16 ? GROUP_16 : GROUP_32;
     if (rows <= 16 || (rows <= 64 && K <= 1024)) return GROUP_64;
-    if (rows > 64 && even_tiles(groups, M, N, GROUP_256) >= 192) return GROUP_256;
+    if (rows >= 384 && even_tiles(groups, M, N, GROUP_256) >= 128) return GROUP_256;
     if (rows > 64 && even_tiles(groups, M, N, GROUP_128x256) >= 192) return GROUP_128x256;
     return even_tiles(groups, M, N, GROUP_128) >= 192 ? GROUP_128 : GROUP_64;
 }

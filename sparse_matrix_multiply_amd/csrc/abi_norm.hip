@@ -77,7 +77,7 @@ mmac_status_t mmac_rmsnorm_grad(mmac_dtype_t x_type, mmac_dtype_t w_type, int64_
     if (dX && ((dX == dY && lddx != lddy) || (dX == dH && lddx != lddh) || dX == H)) return MMAC_ERR_INVALID_ARG;
     if (!aligned(w, 16) || !aligned(rstd, 4) || !aligned(dW, 16) || !aligned(workspace, 16)) return MMAC_ERR_MISALIGNED;
     if (N == 0 || (M == 0 && !dW)) return MMAC_OK;
-    if (dW && (!workspace || workspace_bytes < grad_bytes(M, N))) return MMAC_ERR_SCRATCH;
+    if (dW && (!workspace || workspace_bytes < grad_bytes(M, N))) return MMAC_ERR_INVALID_ARG;
     NormGradParams p{};
     p.dY = static_cast<const uint8_t *>(dY);
     p.dy_pitch = lddy * es;

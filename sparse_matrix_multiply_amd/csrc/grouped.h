@@ -53,14 +53,21 @@ __device__ __forceinline__ int lanes_up_to(int v) {
     return v;
 }
 
+// What is left of a group's rows after whole tiles may take a tile of half the rows where it fits one.
+//   HALF_IN_PLACE  at its place beside the group's other tiles, with which it shares the weights in the L2.
+//   HALF_LAST      after all whole tiles, so that the compute units that are free first at the end find short work; its weights are
+//                  read from memory once more.
+// Measured (bf16, lognormal groups, us in place / last): 256 rows, 20 groups of 300 x 2048 x 4096 166 / 144, 16 of 512 x 4096 x 2048 212
+// / 202, 16 of 1024 x 4096 x 2048 303 / 300; 128 rows, 16 of 256 x 4096 x 4096 213 / 222, 32 of 256 x 2048 x 4096 214 / 233.
+enum : int { HALF_NONE, HALF_IN_PLACE, HALF_LAST };
+
 // Workgroup -> (group, tile), from the offsets alone.  Every wave looks for itself, 64 groups at a time: lane i has group
-// base + i, its number of tile rows, and the sum of those before it.  Tiles are BM rows high; with HALF, what is left of a group
-// after them takes a tile of BM / 2 rows when it fits one, and all of those come last, so that the compute units that are free
-// first at the end find short work.  Either kind is numbered group by group, within a group in bands of group_m tile rows,
-// column by column, and dealt to the XCDs in contiguous runs, so tiles that share a group's weights are in one
-// L2.  Returns false for the workgroups behind the last tile: the host only knows the most tiles there can
-// be.  A range that leaves the arrays is cut to them, a decreasing one is empty.
-template <int BM, bool HALF>
+// base + i, its number of tile rows, and the sum of those before it.  Tiles are BM rows high; whole ones and those of HALF_LAST
+// are numbered each group by group, within a group in bands of group_m tile rows, column by column, and dealt to the
+// XCDs in contiguous runs, so tiles that share a group's weights run at about the same time on one L2.  Returns false
+// for the workgroups behind the last tile: the host only knows the most tiles there can be.  A range that leaves
+// the arrays is cut to them, a decreasing one is empty.
+template <int BM, int HALF>
 __device__ __forceinline__ bool find_group_tile(const Groups &q, int tiles_n, int group_m, int wg, GroupTileAt &at) {
     const int lane = threadIdx.x & 63;
     const auto rows_of = [&](int g, int &first, int &rows) {
@@ -72,21 +79,21 @@ __device__ __forceinline__ bool find_group_tile(const Groups &q, int tiles_n, in
         }
         rows = end - first;
     };
-    const auto whole = [](int rows) { return HALF ? (rows + BM / 2 - 1) / BM : (rows + BM - 1) / BM; };
-    const auto half = [](int rows) { return HALF && rows % BM > 0 && rows % BM <= BM / 2 ? 1 : 0; };
+    const auto whole = [](int rows) { return (rows + (HALF == HALF_LAST ? BM / 2 : BM) - 1) / BM; };
+    const auto half = [](int rows) { return rows % BM > 0 && rows % BM <= BM / 2 ? 1 : 0; };
     int first, rows;
     rows_of(lane, first, rows);
-    const int first0 = first, rows0 = rows, up0 = lanes_up_to(whole(rows)), low0 = HALF ? lanes_up_to(half(rows)) : 0;
-    int total = __builtin_amdgcn_readlane(up0, 63), total_low = HALF ? __builtin_amdgcn_readlane(low0, 63) : 0;
+    const int first0 = first, rows0 = rows, up0 = lanes_up_to(whole(rows)), low0 = HALF == HALF_LAST ? lanes_up_to(half(rows)) : 0;
+    int total = __builtin_amdgcn_readlane(up0, 63), total_low = HALF == HALF_LAST ? __builtin_amdgcn_readlane(low0, 63) : 0;
     for (int base = 64; base < q.count; base += 64) {
         rows_of(base + lane, first, rows);
         total += __builtin_amdgcn_readlane(lanes_up_to(whole(rows)), 63);
-        if (HALF) total_low += __builtin_amdgcn_readlane(lanes_up_to(half(rows)), 63);
+        if (HALF == HALF_LAST) total_low += __builtin_amdgcn_readlane(lanes_up_to(half(rows)), 63);
     }
     const int x = wg & 7;
     int local = wg >> 3, U = total * tiles_n, mine = (U >> 3) + (x < (U & 7) ? 1 : 0);
     at.low = false;
-    if (HALF && local >= mine) {
+    if (HALF == HALF_LAST && local >= mine) {
         local -= mine;
         U = total_low * tiles_n;
         mine = (U >> 3) + (x < (U & 7) ? 1 : 0);
@@ -110,8 +117,10 @@ __device__ __forceinline__ bool find_group_tile(const Groups &q, int tiles_n, in
             const int high = min(count - above, group_m), rest = in - band * per_band;
             at.top = __builtin_amdgcn_readfirstlane(at.low ? at.rows / BM * BM : (above + rest % high) * BM);
             at.tn = __builtin_amdgcn_readfirstlane(rest / high);
+            if (HALF == HALF_IN_PLACE) at.low = at.rows - at.top <= BM / 2;
             at.g = __builtin_amdgcn_readfirstlane(at.g);
-            return true;
+            // holds but for offsets so wrong that the sums above passed 31 bits
+            return (uint32_t)at.top < (uint32_t)at.rows && (uint32_t)at.tn < (uint32_t)tiles_n;
         }
         sum += __builtin_amdgcn_readlane(up, 63);
         base += 64;

@@ -34,7 +34,7 @@ __global__ __launch_bounds__(512) void gemm_grouped_mx_rows_kernel(GemmParams p,
     typedef MxRows<FB> R;
     __shared__ __attribute__((aligned(16))) uint8_t smem[R::kLds];
     GroupTileAt at;
-    if (!find_group_tile<16, false>(q, p.tiles_n, p.group_m, blockIdx.x, at)) return;
+    if (!find_group_tile<16, HALF_NONE>(q, p.tiles_n, p.group_m, blockIdx.x, at)) return;
     take_group(p, q, at, at.top);
     p.M = min(p.M, 16);
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r16 = lane & 15, quarter = lane >> 4;

@@ -9,7 +9,7 @@ template <class Op, int MB, int NSLOT>
 __global__ __launch_bounds__(512) void gemm_grouped_rows_kernel(GemmParams p, Groups q) {
     __shared__ __attribute__((aligned(16))) uint8_t smem[skinny_lds<Op, MB, 1, 8, NSLOT>()];
     GroupTileAt at;
-    if (!find_group_tile<16 * MB, false>(q, p.tiles_n, p.group_m, blockIdx.x, at)) return;
+    if (!find_group_tile<16 * MB, HALF_NONE>(q, p.tiles_n, p.group_m, blockIdx.x, at)) return;
     take_group(p, q, at, at.top);
     p.M = min(p.M, 16 * MB);
     skinny_columns<Op, MB, 1, 8, NSLOT>(p, at.tn, smem);

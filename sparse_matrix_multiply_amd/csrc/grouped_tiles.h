@@ -14,8 +14,8 @@ __device__ __forceinline__ void group_tile(const GemmParams &p, const GroupTileA
     t.epilogue(smem);
 }
 
-// One workgroup per tile of BM x BN, WM x WN waves; HALF: or of BM / 2 x BN, for the last rows of a group.
-template <class Op, int BM, int BN, int WM, int WN, int STAGES, bool HALF, int PER_CU = 1>
+// One workgroup per tile of BM x BN, WM x WN waves, or (HALF) of BM / 2 x BN; PER_CU of them a compute unit.
+template <class Op, int BM, int BN, int WM, int WN, int STAGES, int HALF, int PER_CU = 1>
 __global__ __launch_bounds__(WM *WN * 64) __attribute__((amdgpu_waves_per_eu(WM * WN * PER_CU / 4, WM * WN * PER_CU / 4)))
 void gemm_grouped_kernel(GemmParams p, Groups q) {
     typedef TiledGemm<Op, BM, BN, WM, WN, STAGES> T;
@@ -99,13 +99,13 @@ hipError_t launch_grouped_op(GroupTile tile, const GemmParams &p, const Groups &
     constexpr int L64 = TiledGemm<Op, 64, 64, 2, 2, 2>::LDS_BYTES, L128 = TiledGemm<Op, 128, 128, 2, 2, 2>::LDS_BYTES;
     constexpr int P64 = 160 * 1024 / L64 < 4 ? 160 * 1024 / L64 : 4, P128 = 160 * 1024 / L128 < 3 ? 160 * 1024 / L128 : 3;
     switch (tile) {
-    case GROUP_64: hipLaunchKernelGGL((gemm_grouped_kernel<Op, 64, 64, 2, 2, 2, false, P64>), grid, dim3(256), 0, s, p, g); break;
-    case GROUP_128: hipLaunchKernelGGL((gemm_grouped_kernel<Op, 128, 128, 2, 2, 2, false, P128>), grid, dim3(256), 0, s, p, g); break;
+    case GROUP_64: hipLaunchKernelGGL((gemm_grouped_kernel<Op, 64, 64, 2, 2, 2, HALF_NONE, P64>), grid, dim3(256), 0, s, p, g); break;
+    case GROUP_128: hipLaunchKernelGGL((gemm_grouped_kernel<Op, 128, 128, 2, 2, 2, HALF_NONE, P128>), grid, dim3(256), 0, s, p, g); break;
     // block-scaled products take this tile for groups of up to 128 rows: a half tile would change little
-    case GROUP_128x256: hipLaunchKernelGGL((gemm_grouped_kernel<Op, 128, 256, 2, 4, 3, !Op::kScaled>), grid, dim3(512), 0, s, p, g); break;
+    case GROUP_128x256: hipLaunchKernelGGL((gemm_grouped_kernel<Op, 128, 256, 2, 4, 3, Op::kScaled ? HALF_NONE : HALF_IN_PLACE>), grid, dim3(512), 0, s, p, g); break;
     case GROUP_256:
         if constexpr (Op::kScaled) return hipErrorInvalidValue;   // no registers left for the scale words
-        else hipLaunchKernelGGL((gemm_grouped_kernel<Op, 256, 256, 2, 4, 2, true>), grid, dim3(512), 0, s, p, g);
+        else hipLaunchKernelGGL((gemm_grouped_kernel<Op, 256, 256, 2, 4, 2, HALF_LAST>), grid, dim3(512), 0, s, p, g);
         break;
     default: return hipErrorInvalidValue;
     }

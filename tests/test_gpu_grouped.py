@@ -31,6 +31,7 @@ ROWS = {
     "all_in_one": ([0, 300, 0], 0, 0),
     "long": ([257, 0, 513], 1, 2),
     "many": ([0, 1, 3, 0, 2] * 27, 0, 1),
+    "many_long": ([0, 70, 3, 0, 140] * 27, 2, 0),
 }
 
 
@@ -114,7 +115,7 @@ def test_forward(t, trans, rows, N, K):
 def test_every_tile_exact(tile, trans, K, monkeypatch):
     """Each tile shape on groups of every size, all epilogue terms, bit for bit on small integers."""
     monkeypatch.setenv("MMAC_TILE", str(tile))
-    for k, rows in enumerate(("uneven", "edges", "long", "many", "none")):
+    for k, rows in enumerate(("uneven", "edges", "long", "many", "none", "many_long")):
         run_forward(ROWS[rows], 270 if k % 2 else 263, K, torch.bfloat16, trans=trans, integers=True, bias=k % 2 == 0, relu=k == 1,
                     alpha=[1.0, 2.0, -1.0][k % 3], beta=[0.0, 1.0, 2.0][k % 3])
 
@@ -126,6 +127,34 @@ def test_epilogue(out, tile, monkeypatch):
     run_forward(ROWS["uneven"], 72, 96, torch.float16, out=OUT[out], bias=True, relu=True, alpha=0.5, beta=-0.25)
     run_forward(ROWS["few"], 71, 96, torch.float16, out=OUT[out], beta=1.0)
     run_forward(ROWS["few"], 64, 0, torch.float16, out=OUT[out], bias=True, beta=2.0)
+
+
+@pytest.mark.parametrize("out", list(OUT))
+@pytest.mark.parametrize("tile", [16, 64, 128, 256])
+def test_outputs_of_any_alignment(out, tile, monkeypatch):
+    """C and D of odd pitches that start at odd elements: the wide accesses at any address, and nothing beside the matrix written."""
+    monkeypatch.setenv("MMAC_TILE", str(tile))
+    sizes, before, behind = ROWS["uneven"]
+    g = rng("odd", out, tile)
+    o, M = offsets(sizes, before, behind)
+    t = OUT[out]
+    for N in (135, 270):
+        a, b, c = g.integers(-2, 3, (M, 64)), g.integers(-2, 3, (len(sizes), N, 64)), g.integers(-2, 3, (M, N))
+        buf = torch.full((M + 2, N + 4), 5.0, device=dev()).to(t)
+        if buf.shape[1] % 2 == 0:
+            buf = torch.full((M + 2, N + 5), 5.0, device=dev()).to(t)
+        D = buf[1:M + 1, 1:N + 1]
+        C = torch.zeros(M, N + 3 + N % 2, device=dev()).to(t)[:, 1:N + 1]
+        C.copy_(torch.from_numpy(c.astype(np.float64)).to(dev()).to(t))
+        mm.gemm_grouped(pitched(a.astype(np.float64), torch.bfloat16), torch.from_numpy(o).to(dev()), matrices(b.astype(np.float64), torch.bfloat16), D,
+                        alpha=0.5, beta=2.0, C=C)
+        torch.cuda.synchronize()
+        host, got = buf.float().cpu(), f64(D.float())
+        assert (host[0] == 5).all() and (host[-1] == 5).all() and (host[:, 0] == 5).all() and (host[:, N + 1:] == 5).all(), "guard cells"
+        for i in range(len(sizes)):
+            r = slice(o[i], o[i + 1])
+            want = torch.from_numpy(0.5 * (a[r] @ b[i].T) + 2.0 * c[r]).to(t).double().numpy()
+            assert np.array_equal(got[r], want), f"group {i}"
 
 
 def test_the_skinny_products_bits():

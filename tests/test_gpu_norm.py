@@ -176,7 +176,6 @@ def test_in_place(N):
         return pitched(f64(x), t)
 
     x, r = again(X), again(Rs)
-    y = torch.empty_like(Y)
     y = pitched(np.zeros((M, N)), t)
     mm.rmsnorm(x, w, y, residual=r, H=r)
     assert torch.equal(r, H) and torch.equal(y, Y) and torch.equal(x, X)
@@ -200,8 +199,7 @@ def test_rows_apart(N):
     x[7] = 1e30
     X = pitched(x, t)
     w = torch.ones(N, device=dev())
-    out, want = torch.empty_like(X), torch.empty_like(X)
-    out, want = pitched(x * 0 + 3, t), pitched(x * 0 + 3, t)
+    out, want = pitched(np.full((M, N), 3.0), t), pitched(np.full((M, N), 3.0), t)
     mm.rmsnorm(X, w, out)
     mm.rmsnorm(clean, w, want)
     for i in (0, 2, 5, 8):
@@ -251,7 +249,6 @@ def test_gradients(t, M, N):
     assert (np.abs(f64(dX) - dx) <= tol + (0 if t is torch.float32 else half_step(np.abs(dx) + tol, t)) + TINY[t]).all()
     # sums over at most ceil(M / parts) rows in turn, 4 waves, ceil(parts / 16) and 16 partial sums; 3 roundings a term
     assert (np.abs(f64(wbuf[:N]) - dw) <= (-(-M // 128) + 60) * U * dwmags + 1e-45).all()
-    plain = torch.zeros_like(dX)
     plain = pitched(np.zeros((M, N)), t)
     mm.rmsnorm_grad(dY, H, w, rstd, plain, dH=dH)        # without dW, without a workspace
     assert torch.equal(plain, dX)

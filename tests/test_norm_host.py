@@ -11,7 +11,7 @@ import sparse_matrix_multiply_amd as mm
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 P = 1 << 20          # a fake, 16-byte aligned "device pointer": never dereferenced here
-OK, INV, UNS, MIS, SCR = mm.OK, mm.ERR_INVALID_ARG, mm.ERR_UNSUPPORTED, mm.ERR_MISALIGNED, mm.ERR_SCRATCH
+OK, INV, UNS, MIS = mm.OK, mm.ERR_INVALID_ARG, mm.ERR_UNSUPPORTED, mm.ERR_MISALIGNED
 BIG = (1 << 63) - 1
 
 
@@ -76,7 +76,7 @@ def grad(L, **kw):
     (dict(dH=P, lddh=60), INV), (dict(lddy=68), MIS), (dict(H=P + 8), MIS), (dict(dX=3 * P + 2), MIS), (dict(W=P + 4), MIS),
     (dict(rstd=P + 1), MIS), (dict(lddx=1 << 23), UNS), (dict(dX=P, lddx=72), INV), (dict(dH=4 * P, lddh=64, dX=4 * P, lddx=72), INV),
     (dict(dX=2 * P), INV), (dict(n=-1), INV), (dict(dW=P + 8, ws=P, n=1 << 30), MIS), (dict(dW=P, ws=P + 8, n=1 << 30), MIS),
-    (dict(dW=P), SCR), (dict(dW=P, ws=P, n=1024), SCR), (dict(M=0, dW=P), SCR),
+    (dict(dW=P), INV), (dict(dW=P, ws=P, n=1024), INV), (dict(M=0, dW=P), INV),
 ])
 def test_rmsnorm_grad_argument_errors(L, kw, code):
     assert grad(L, **kw) == code
@@ -90,7 +90,7 @@ def test_rmsnorm_grad_empty_and_workspace(L):
     for M, N in ((0, 8), (1, 8), (5000, 64), (1 << 30, 4096)):
         n = mm.rmsnorm_grad_workspace_bytes(M, N)
         assert n >= 1024 + 4 * N and (n - 1024) % (4 * N) == 0 and n <= 1024 + 512 * 4 * N
-        assert grad(L, M=M, N=N, lddy=N, ldh=N, lddx=N, dW=P, ws=P, n=n - 1) == SCR
+        assert grad(L, M=M, N=N, lddy=N, ldh=N, lddx=N, dW=P, ws=P, n=n - 1) == INV
 
 
 def quantize(L, **kw):
