@@ -11,6 +11,10 @@
 // 16q .. 16q + 15 and 64 + 16q .. 64 + 16q + 15, 4-bit elements 32q .. 32q + 31; its scale operand's byte 0 is the exponent of
 // elements 32q .. 32q + 31 in either format.  Established on gfx950 by the products' agreement with the 64-bit sums, every block's
 // exponent and every element different; the parity tests recheck it.
+//
+// Measured: 16 rows through 16 experts of 4096 x 4096 FP4 (143 MB) in 31.7 us (4.5 TB/s).  With A and its scale words in the ring too,
+// so that one workgroup filled a compute unit's LDS, 42 us: at K 4096 a wave's range is its two slots, and nothing ran
+// while a workgroup started or ended.
 #include "grouped.h"
 #include "skinny.h"
 

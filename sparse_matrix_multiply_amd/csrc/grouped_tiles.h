@@ -1,4 +1,9 @@
 // Grouped products in tiles: the tiled kernel's main loop and epilogue on one group's part of the arrays.
+//
+// Each tile is the dense kernel's, so what bounds it is the same (matrix instructions and the copies that feed them); what is the
+// groups' own is the tiles that their last rows leave partly empty, the rounds of tiles, and weights that only two or three
+// tile rows share.  8192 rows, 4096 x 4096 bf16: one or two groups 225 to 230 us (1200 TFLOP/s), 16 equal ones 256, 16 of
+// lognormal sizes 324 to 331.
 #pragma once
 
 #include "gemm_tiled.h"
