@@ -5,7 +5,7 @@
  * memory, asynchrony, errors, thread safety, alpha and beta) hold here too; an
  * operand without elements may be NULL.
  *
- *   groups   their number G, 1 or more.
+ *   groups   their number G, at most 2^30 (MMAC_ERR_UNSUPPORTED beyond).
  *   offsets  G + 1 32-bit integers in device memory, not decreasing, from 0 to M:
  *            rows offsets[g] .. offsets[g+1] - 1 belong to group g, which may have none.
  *            Rows before offsets[0] and from offsets[G] on belong to no group: they are

@@ -11,6 +11,8 @@ using namespace mmac;
 
 namespace {
 
+constexpr int64_t kMaxGroups = 1 << 30;   // the search for a tile counts them in 32 bits, 256 at a time
+
 int forced_tile() {
     const char *s = std::getenv("MMAC_TILE");
     switch (s ? std::atoi(s) : 0) {
@@ -85,6 +87,7 @@ int64_t most_tiles(int64_t groups, int64_t M, int rows, int64_t columns) {
 // What the products share: dimensions, alpha ... D and the epilogue, offsets.
 mmac_status_t check_common(int64_t groups, int64_t M, int64_t N, int64_t K, const int32_t *offsets) {
     if (bad_dim(groups) || bad_dim(M) || bad_dim(N) || bad_dim(K)) return MMAC_ERR_INVALID_ARG;
+    if (groups > kMaxGroups) return MMAC_ERR_UNSUPPORTED;
     if (groups > 0 && M > 0 && N > 0 && !offsets) return MMAC_ERR_INVALID_ARG;
     return aligned(offsets, 4) ? MMAC_OK : MMAC_ERR_MISALIGNED;
 }
@@ -241,6 +244,7 @@ mmac_status_t mmac_gemm_grouped_wgrad(mmac_dtype_t y_type, int64_t groups, int64
     const mmac_epilogue_t ep = epilogue_of(ep_in);
     if (!is_16bit(y_type)) return MMAC_ERR_UNSUPPORTED;
     if (bad_dim(groups) || bad_dim(M) || bad_dim(N) || bad_dim(K)) return MMAC_ERR_INVALID_ARG;
+    if (groups > kMaxGroups) return MMAC_ERR_UNSUPPORTED;
     const bool empty = groups == 0 || N == 0 || K == 0;
     if (!empty && (!offsets || (M > 0 && (!dY || !X)))) return MMAC_ERR_INVALID_ARG;
     mmac_status_t st = check_out(groups > 0 ? N : 0, K, alpha, beta, C, ldc, D, ldd, ep);

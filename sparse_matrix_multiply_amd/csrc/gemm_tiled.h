@@ -906,7 +906,7 @@ struct TiledGemm {
     // elements per load), ReLU and the rounding, in a loop unrolled only four
     // times (one short body per output type, four C loads in flight).  Four outputs leave in one
     // 8-byte (16-bit D) or 4-byte (8-bit D) store, at any alignment (24 bf16 matrices of 5786 x 1891 from one row
-    // each, the weight gradient of a grouped product: 1771 us with elements one by one, 130 us so).
+    // each, the weight gradient of a grouped product: 1771 us with elements one by one, 168 so).
     __device__ __forceinline__ void epilogue_converted(uint8_t *smem) {
         if constexpr (std::is_same<out_t, float>::value) {
             switch (p.d_type) {   // one copy of the loops per output type

@@ -32,6 +32,7 @@ ROWS = {
     "long": ([257, 0, 513], 1, 2),
     "many": ([0, 1, 3, 0, 2] * 27, 0, 1),
     "many_long": ([0, 70, 3, 0, 140] * 27, 2, 0),
+    "crowd": ([1, 0, 2] * 90 + [150, 0, 20] * 3, 1, 0),
 }
 
 
@@ -115,7 +116,7 @@ def test_forward(t, trans, rows, N, K):
 def test_every_tile_exact(tile, trans, K, monkeypatch):
     """Each tile shape on groups of every size, all epilogue terms, bit for bit on small integers."""
     monkeypatch.setenv("MMAC_TILE", str(tile))
-    for k, rows in enumerate(("uneven", "edges", "long", "many", "none", "many_long")):
+    for k, rows in enumerate(("uneven", "edges", "long", "many", "none", "many_long", "crowd")):
         run_forward(ROWS[rows], 270 if k % 2 else 263, K, torch.bfloat16, trans=trans, integers=True, bias=k % 2 == 0, relu=k == 1,
                     alpha=[1.0, 2.0, -1.0][k % 3], beta=[0.0, 1.0, 2.0][k % 3])
 

@@ -61,7 +61,7 @@ OUT = [
     (dict(D=None), INV), (dict(ldd=1), INV), (dict(beta=1.0), INV), (dict(alpha=float("nan")), INV),
     (dict(beta=float("inf"), C=P, ldc=128), INV), (dict(alpha=1e39), INV), (dict(D=P + 2), MIS), (dict(ldd=1 << 22), UNS),
     (dict(beta=1.0, C=P, ldc=10), INV), (dict(ep=mm.Epilogue(9, 0, None)), INV), (dict(ep=mm.Epilogue(0, 7, None)), INV),
-    (dict(G=-1), INV), (dict(G=1 << 31), INV), (dict(M=-1), INV), (dict(N=1 << 31), INV), (dict(K=-1), INV), (dict(off=None), INV), (dict(off=P + 2), MIS),
+    (dict(G=-1), INV), (dict(G=1 << 31), INV), (dict(G=(1 << 30) + 1), UNS), (dict(M=-1), INV), (dict(N=1 << 31), INV), (dict(K=-1), INV), (dict(off=None), INV), (dict(off=P + 2), MIS),
 ]
 
 
