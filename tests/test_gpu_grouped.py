@@ -400,6 +400,83 @@ def test_mx_fp32_outputs_are_exact_to_fp32(tile, monkeypatch):
     run_mx(ROWS["edges"], 64, 4096, "e5m2", "fp4", torch.float32)
 
 
+@pytest.mark.parametrize("tile", [16, 64, 128, 1282])
+@pytest.mark.parametrize("kb", ["e4m3", "e5m2", "fp4"])
+@pytest.mark.parametrize("out", ["bf16", "fp16"])
+@pytest.mark.parametrize("K", [704, 1024])
+def test_mx_every_tile_exact_in_16_bits(tile, kb, out, K, monkeypatch):
+    """The block-scaled instructions over many k-tiles: every sum is a multiple of 1/4 below 2^17, exact in any order, and the output
+    its nearest value, bit for bit."""
+    monkeypatch.setenv("MMAC_TILE", str(tile))
+    for k, rows in enumerate(("edges", "uneven", "long")):
+        run_mx(ROWS[rows], 70 if k == 2 else 263, K, ["e4m3", "e5m2"][k % 2], kb, OUT[out], integers=True, bias=k == 1, pad=k % 2)
+
+
+@pytest.mark.parametrize("tile", [16, 64, 128, 1282])
+@pytest.mark.parametrize("ka", ["e4m3", "e5m2"])
+@pytest.mark.parametrize("kb", ["e4m3", "e5m2", "fp4"])
+@pytest.mark.parametrize("K", [512, 1120, 4096])
+def test_mx_16_bit_outputs_in_every_tile(tile, ka, kb, K, monkeypatch):
+    monkeypatch.setenv("MMAC_TILE", str(tile))
+    run_mx(ROWS["edges"], 130, K, ka, kb, torch.bfloat16)
+    run_mx(ROWS["long"], 70, K, ka, kb, torch.float16, beta=1.0)
+
+
+def scaled(c, e, kind):
+    """Values of codes (rows x K) with a scale per 32."""
+    pos, sign = (R.E2M1, 8) if kind == "fp4" else (R.E4M3_POS, 128)
+    return np.where(c >= sign, -1.0, 1.0) * pos[c % sign] * np.repeat(np.ldexp(1.0, e.astype(np.int64) - 127), 32, 1)
+
+
+def run_mx_codes(ca, ea, cb, eb, kb, out):
+    """One group's product of given codes (A E4M3): its values, the sums in 64 bits and those of the magnitudes."""
+    A = torch.from_numpy(ca.astype(np.uint8)).to(dev()).view(torch.float8_e4m3fn)
+    packed = (cb[:, 0::2] | (cb[:, 1::2] << 4)) if kb == "fp4" else cb
+    B = torch.from_numpy(packed.astype(np.uint8)).to(dev()).unsqueeze(0)
+    B = B if kb == "fp4" else B.view(torch.float8_e4m3fn)
+    SA, SB = (torch.from_numpy(R.sx_words(e, 127)).to(dev()) for e in (ea, eb))
+    D = torch.empty(len(ca), len(cb), dtype=out, device=dev())
+    mm.gemm_grouped_mx(A, SA, torch.tensor([0, len(ca)], dtype=torch.int32, device=dev()), B, SB.unsqueeze(0), D,
+                       b_type=mm.FP4_E2M1 if kb == "fp4" else None)
+    a, b = scaled(ca, ea, "e4m3"), scaled(cb, eb, kb)
+    return f64(D), a @ b.T, np.abs(a) @ np.abs(b.T)
+
+
+@pytest.mark.parametrize("tile", [16, 64, 128, 1282])
+@pytest.mark.parametrize("kb", ["e4m3", "fp4"])
+@pytest.mark.parametrize("out", list(OUT))
+def test_mx_sums_that_cancel(tile, kb, out, monkeypatch):
+    """The second half of K takes back the first but for one block, so a result is some thousandths of the magnitudes: within 2^-13
+    of those (outputs of 16 bits or fewer; fp32 ones without that) and the output's half step."""
+    monkeypatch.setenv("MMAC_TILE", str(tile))
+    g = rng("cancel", kb)
+    K, M, N = 2048, 70, 96
+    ca, cb = g.integers(0, 0x60, (M, K)) + 128 * g.integers(0, 2, (M, K)), g.integers(0, 8 if kb == "fp4" else 0x60, (N, K))
+    ea, eb = 127 + g.integers(-3, 4, (M, K // 32)), 127 + g.integers(-3, 4, (N, K // 32))
+    h, q = K // 2, K // 64
+    ca[:, h:], cb[:, h:], ea[:, q:], eb[:, q:] = ca[:, :h] ^ 128, cb[:, :h], ea[:, :q], eb[:, :q]
+    ea[:, -1] -= 4
+    got, want, mags = run_mx_codes(ca, ea, cb, eb, kb, OUT[out])
+    assert np.median(np.abs(want) / mags) < 2.0 ** -6
+    check_sums(got, want, mags, K, OUT[out], 0.0 if out == "fp32" else 2.0 ** -13)
+
+
+@pytest.mark.parametrize("tile", [16, 64, 128, 1282])
+@pytest.mark.parametrize("kb", ["e4m3", "fp4"])
+@pytest.mark.parametrize("out", ["bf16", "fp16"])
+def test_mx_exponents_far_apart(tile, kb, out, monkeypatch):
+    """Scales near the ends of their range that meet their opposites: the products, of the size of one, count in 16-bit outputs."""
+    monkeypatch.setenv("MMAC_TILE", str(tile))
+    g = rng("far apart", kb)
+    K, M, N = 512, 70, 96
+    ca, cb = g.integers(0, 0x60, (M, K)) + 128 * g.integers(0, 2, (M, K)), g.integers(0, 8 if kb == "fp4" else 0x60, (N, K))
+    low = g.integers(0, 2, K // 32).astype(bool)
+    ea, eb = g.integers(1, 4, (M, K // 32)), g.integers(250, 253, (N, K // 32))
+    ea, eb = np.where(low, ea, 254 - ea), np.where(low, eb, 254 - eb)
+    got, want, mags = run_mx_codes(ca, ea, cb, eb, kb, OUT[out])
+    check_sums(got, want, mags, K, OUT[out], 2.0 ** -13)
+
+
 def test_mx_of_zero_length():
     D = torch.full((4, 8), 5.0, device=dev())
     e = torch.empty(4, 0, dtype=torch.float8_e4m3fn, device=dev())
