@@ -56,7 +56,7 @@ mmac_status_t mmac_rmsnorm(mmac_dtype_t x_type, mmac_dtype_t w_type, mmac_dtype_
  *             without dW.  It need not be cleared, and its first KiB is left alone, so
  *             it may be a workspace that the products share, in one stream.
  * dX may be dY or dH (with the same pitch).  The sums are added up in a fixed order:
- * the results do not depend on timing.  M == 0: dW is zero.  N == 0: nothing is done.
+ * the results do not depend on timing.  M == 0: dW is zero, and only that is done.  N == 0: nothing is done.
  */
 mmac_status_t mmac_rmsnorm_grad(mmac_dtype_t x_type, mmac_dtype_t w_type, int64_t M, int64_t N, const void *dY,
                                 int64_t lddy, const void *H, int64_t ldh, const void *w, const float *rstd,

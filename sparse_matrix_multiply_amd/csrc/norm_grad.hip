@@ -200,9 +200,11 @@ int norm_grad_parts(int64_t M, int64_t N) {
 
 template <int XT, int WT>
 static hipError_t launch_as(const NormGradParams &p, hipStream_t s) {
-    const int parts = norm_grad_parts(p.M, p.N);
+    // without rows there are no partial sums, and nothing to read: only dW, which is zero, is written
+    const int parts = p.M > 0 ? norm_grad_parts(p.M, p.N) : 0;
     const dim3 grid(parts);
-    if (p.N <= 512) hipLaunchKernelGGL((rmsnorm_grad_kernel<XT, WT, 64, 1>), grid, dim3(256), 0, s, p);
+    if (parts == 0) {}
+    else if (p.N <= 512) hipLaunchKernelGGL((rmsnorm_grad_kernel<XT, WT, 64, 1>), grid, dim3(256), 0, s, p);
     else if (p.N <= 1024) hipLaunchKernelGGL((rmsnorm_grad_kernel<XT, WT, 64, 2>), grid, dim3(256), 0, s, p);
     else if (p.N <= 2048) hipLaunchKernelGGL((rmsnorm_grad_kernel<XT, WT, 256, 1>), grid, dim3(256), 0, s, p);
     else if (p.N <= 4096) hipLaunchKernelGGL((rmsnorm_grad_kernel<XT, WT, 512, 1>), grid, dim3(512), 0, s, p);

@@ -268,6 +268,27 @@ def test_gradient_without_rows():
     assert (dW == 0).all()
 
 
+@pytest.mark.parametrize("N", [40, 1500, 9000, 16384, 16388, 40000])
+def test_gradient_without_rows_reads_no_workspace(N):
+    """dW is zero whatever the workspace holds, in every kernel's range of N; and so without the pointers that no row needs."""
+    ws = torch.full_like(mm.rmsnorm_grad_workspace(0, N, dev()), 255)
+    z, w, r = torch.empty(0, N, device=dev()), torch.ones(N, device=dev()), torch.empty(0, device=dev())
+    dW = torch.full((N + 4,), 5.0, device=dev())
+    mm.rmsnorm_grad(z, z, w, r, z, dW=dW[:N], workspace=ws)
+    assert (dW[:N] == 0).all() and (dW[N:] == 5).all()
+
+
+@pytest.mark.parametrize("N", [40, 1500, 9000, 16384, 16388, 40000])
+def test_gradient_without_rows_or_pointers(N):
+    ws = torch.full_like(mm.rmsnorm_grad_workspace(0, N, dev()), 255)
+    dW = torch.full((N,), 5.0, device=dev())
+    ld = -(-N // 8) * 8
+    assert mm.raw_call("mmac_rmsnorm_grad", mm.BF16, mm.F32, 0, N, None, ld, None, ld, None, None, None, 0, None, ld, dW.data_ptr(),
+                       ws.data_ptr(), ws.numel(), torch.cuda.current_stream().cuda_stream) == mm.OK
+    torch.cuda.synchronize()
+    assert (dW == 0).all() and (ws == 255).all()
+
+
 @pytest.mark.parametrize("N", [40, 1500])
 def test_gradients_by_differences(N):
     """The forward pass's central differences along random directions (in 64 bits) against the kernels' gradients: the formula's
