@@ -73,7 +73,8 @@ mmac_status_t mmac_gemm_grouped_mx(mmac_dtype_t a_type, mmac_dtype_t b_type, int
  *   D, C      group g's matrix is at D + g * stride_d (C + g * stride_c) elements;
  *             stride_d >= (N - 1) * ldd + K.
  *   ep        NULL, or d_type with act NONE and bias NULL (MMAC_ERR_UNSUPPORTED otherwise).
- * A group without rows: D_g = beta * C_g.  Rows of no group do not count.
+ * A group without rows: D_g = beta * C_g.  Rows of no group do not count.  More than 4 million
+ * tiles of 256 x 256 (each group's counted up to whole ones): MMAC_ERR_UNSUPPORTED.
  */
 mmac_status_t mmac_gemm_grouped_wgrad(mmac_dtype_t y_type, int64_t groups, int64_t M, int64_t N, int64_t K,
                                       double alpha, const void *dY, int64_t ldy, const void *X, int64_t ldx,

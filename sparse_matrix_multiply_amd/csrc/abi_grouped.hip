@@ -77,6 +77,9 @@ GroupTile wgrad_tile(int64_t groups, int64_t M, int64_t N, int64_t K, int64_t ti
     return GROUP_64;
 }
 
+// A launch counts its threads in 32 bits; half of that is enough here.
+bool grid_fits(int64_t blocks, GroupTile t) { return blocks <= INT32_MAX / group_threads(t); }
+
 // The most tiles that M rows in `groups` groups can make: n groups with rows, all but one row of each spread evenly
 // (a half tile counts as one).
 int64_t most_tiles(int64_t groups, int64_t M, int rows, int64_t columns) {
@@ -259,11 +262,13 @@ mmac_status_t mmac_gemm_grouped_wgrad(mmac_dtype_t y_type, int64_t groups, int64
     if (!aligned(offsets, 4)) return MMAC_ERR_MISALIGNED;
     if (empty) return MMAC_OK;
 
-    const auto tiles = [&](GroupTile t) { return groups * ((N + group_rows(t) - 1) / group_rows(t)) * ((K + group_cols(t) - 1) / group_cols(t)); };
+    const auto per = [&](GroupTile t) { return ((N + group_rows(t) - 1) / group_rows(t)) * ((K + group_cols(t) - 1) / group_cols(t)); };
     const int forced = forced_tile();
-    GroupTile t = forced >= 0 ? (GroupTile)forced : wgrad_tile(groups, M, N, K, tiles(GROUP_256), ep.d_type == MMAC_OUT_ACC);
+    GroupTile t = forced >= 0 ? (GroupTile)forced : wgrad_tile(groups, M, N, K, groups * per(GROUP_256), ep.d_type == MMAC_OUT_ACC);
     if (t == GROUP_16 || t == GROUP_32) t = GROUP_64;
-    if (tiles(t) > INT32_MAX / 1024 / 8) return MMAC_ERR_UNSUPPORTED;   // the grid, with up to 7 idle workgroups a group
+    // so many tiles that only larger ones can be launched
+    while (t != GROUP_256 && !grid_fits(wgrad_blocks(per(t), groups), t)) t = t == GROUP_64 ? GROUP_128 : GROUP_256;
+    if (!grid_fits(wgrad_blocks(per(t), groups), t)) return MMAC_ERR_UNSUPPORTED;
     GemmParams p = make_params(N, K, 0, alpha, dY, ldy * 2, X, ldx * 2, beta, C, ldc, D, ldd, ep);
     p.tiles_m = (int)((N + group_rows(t) - 1) / group_rows(t));
     p.tiles_n = (int)((K + group_cols(t) - 1) / group_cols(t));

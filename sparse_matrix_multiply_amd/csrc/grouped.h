@@ -26,6 +26,9 @@ inline int group_rows(GroupTile t) {
 inline int group_cols(GroupTile t) {
     return t == GROUP_16 || t == GROUP_32 ? 16 : t == GROUP_64 ? 64 : t == GROUP_128 ? 128 : 256;
 }
+inline int group_threads(GroupTile t) { return t == GROUP_64 || t == GROUP_128 ? 256 : 512; }
+// Workgroups of the weight gradient: `per` tiles a group, which share them out to the XCDs where there are some for each.
+inline int64_t wgrad_blocks(int64_t per, int64_t groups) { return (per >= 64 ? (per + 7) / 8 * 8 : per) * groups; }
 // Columns of a workgroup of the block-scaled kernels that stream the weights.
 constexpr int kMxRowsCols = 32;
 

@@ -119,8 +119,7 @@ hipError_t launch_grouped_op(GroupTile tile, const GemmParams &p, const Groups &
 
 template <class Op>
 hipError_t launch_grouped_wgrad_op(GroupTile tile, const GemmParams &p, const Groups &g, hipStream_t s) {
-    const int64_t per = (int64_t)p.tiles_m * p.tiles_n;
-    const dim3 grid((unsigned)(per >= 64 ? (per + 7) / 8 * 8 * g.count : per * g.count));   // as the kernel counts
+    const dim3 grid((unsigned)wgrad_blocks((int64_t)p.tiles_m * p.tiles_n, g.count));   // as the kernel counts
     switch (tile) {
     case GROUP_64: hipLaunchKernelGGL((gemm_grouped_wgrad_kernel<Op, 64, 64, 2, 2, 2, 5>), grid, dim3(256), 0, s, p, g); break;
     case GROUP_128: hipLaunchKernelGGL((gemm_grouped_wgrad_kernel<Op, 128, 128, 2, 2, 2, 2>), grid, dim3(256), 0, s, p, g); break;

@@ -261,6 +261,23 @@ def test_wgrad_outputs(out):
     run_wgrad(ROWS["few"], 33, 65, torch.float16, out=OUT[out], beta=1.0, same=True)
 
 
+@pytest.mark.parametrize("G,N,K", [(256, 1100, 7168), (300_000, 65, 80), (4200, 4100, 66)])
+def test_wgrad_of_many_tiles(G, N, K):
+    """More workgroups than 2^18 of them: every group's matrix is written, those without rows with zeros."""
+    g = rng("many tiles", G)
+    sizes = np.zeros(G, int)
+    sizes[g.integers(0, G, 40)], sizes[0], sizes[-1] = 3, 2, 5
+    o, M = offsets(sizes, 0, 0)
+    dy, x = g.integers(-2, 3, (M, N)).astype(np.float64), g.integers(-2, 3, (M, K)).astype(np.float64)
+    D = torch.full((G, N, K), 5.0, dtype=torch.bfloat16, device=dev())            # 4.0, 3.1 and 2.3 GB
+    mm.gemm_grouped_wgrad(pitched(dy, torch.bfloat16), pitched(x, torch.bfloat16), torch.from_numpy(o).to(dev()), D)
+    some = sizes > 0
+    for i in np.flatnonzero(some):
+        assert np.array_equal(f64(D[i]), dy[o[i]:o[i + 1]].T @ x[o[i]:o[i + 1]]), f"group {i}"
+    written = (D.view(G, -1) == 0).all(1).cpu().numpy()
+    assert written[~some].all()
+
+
 def test_wgrad_rows_past_one_descriptor():
     """A pitch so wide that one buffer descriptor covers 255 rows (192 are walked at a time): the parts add up, exactly."""
     M, N, K, ld = 700, 40, 72, 1 << 22

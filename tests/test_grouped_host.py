@@ -98,6 +98,21 @@ def test_gemm_grouped_wgrad_argument_errors(L, kw, code):
     assert wgrad(L, **kw) == code
 
 
+# On a machine without a GPU the launch itself is what fails: the call was not refused.
+no_gpu = pytest.mark.skipif(torch.cuda.is_available(), reason="the pointers are fake: the calls would run")
+
+
+@no_gpu
+@pytest.mark.parametrize("kw", [
+    dict(G=384, M=65536, N=2048, K=7168), dict(G=256, M=300, N=1100, K=7168, ep=mm.Epilogue(2, 0, None)), dict(G=300_000, M=300_000, N=16, K=16),
+    dict(G=100_000, M=300, N=1000, K=1000, ep=mm.Epilogue(2, 0, None)), dict(G=60_000, M=300, N=1000, K=1000),
+])
+def test_wgrad_of_many_tiles_is_not_refused(L, kw):
+    """Matrices that fit the GPU's memory: any of the tiles' grids that fits will do."""
+    N, K = kw["N"], kw["K"]
+    assert wgrad(L, ldy=-(-N // 8) * 8, ldx=-(-K // 8) * 8, ldd=K, sd=N * K, **kw) == mm.ERR_HIP
+
+
 def test_empty_is_a_no_op(L):
     for kw in (dict(G=0), dict(M=0), dict(N=0)):
         assert grouped(L, A=None, B=None, D=None, off=None, **kw) == OK
