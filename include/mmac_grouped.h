@@ -36,7 +36,9 @@ extern "C" {
  *             K x N (K rows of N elements, ldb >= N, K * ldb * 2 below 2^31 bytes): with the
  *             same weights, their N as this K, the gradient of the forward product's input.
  *   A, C, D   M rows; ep as in mmac_gemm_dense_ep, but ep->bias holds G rows of N values.
- * M, N or G == 0: nothing is done.  K == 0: the sum is zero (A and B are not read).
+ * M, N or G == 0: nothing is done.  K == 0: the sum is zero (A and B are not read).  More than
+ * 4 million tiles of 256 x 256 (128 x 256 in mmac_gemm_grouped_mx), each group's counted
+ * up to whole ones in the worst spread of the rows: MMAC_ERR_UNSUPPORTED.
  */
 mmac_status_t mmac_gemm_grouped(mmac_dtype_t a_type, int trans_b, int64_t groups, int64_t M, int64_t N, int64_t K,
                                 double alpha, const void *A, int64_t lda, const int32_t *offsets, const void *B,

@@ -137,14 +137,23 @@ GemmParams make_params(int64_t M, int64_t N, int64_t K, double alpha, const void
     return p;
 }
 
-// Tile counts of the forward products and their grid; false if it would pass a 32-bit count of threads.
-bool set_grid(GemmParams &p, int64_t groups, int rows, int cols, int64_t &grid) {
-    const int64_t tn = (p.N + cols - 1) / cols;
-    grid = (most_tiles(groups, p.M, rows, tn) + 7) / 8 * 8 + 8;   // either kind of tile may leave some XCDs one short
-    if (tn > INT32_MAX / 1024 || grid > INT32_MAX / 1024) return false;
-    p.tiles_n = (int)tn;
-    p.tiles_m = 0;   // differs by group
-    return true;
+constexpr GroupTile kMxLargest = GROUP_128x256;   // of the block-scaled products
+
+// Tile counts of the forward products and their grid.  Where that is too large to launch, larger tiles up to `largest` take the
+// place of t; false if none fits.
+bool set_grid(GemmParams &p, int64_t groups, GroupTile &t, GroupTile largest, int64_t &grid) {
+    for (;;) {
+        const int cols = largest == kMxLargest && t == GROUP_16 ? kMxRowsCols : group_cols(t);
+        const int64_t tn = (p.N + (int64_t)cols - 1) / cols;
+        grid = (most_tiles(groups, p.M, group_rows(t), tn) + 7) / 8 * 8 + 8;   // either kind of tile may leave some XCDs one short
+        if (grid_fits(grid, t)) {
+            p.tiles_n = (int)tn;
+            p.tiles_m = 0;   // differs by group
+            return true;
+        }
+        if (t >= largest) return false;
+        t = t < GROUP_64 ? GROUP_64 : t == GROUP_64 ? GROUP_128 : largest;
+    }
 }
 
 }  // namespace
@@ -184,7 +193,7 @@ mmac_status_t mmac_gemm_grouped(mmac_dtype_t a_type, int trans_b, int64_t groups
     g.b_stride = groups > 1 ? stride_b * 2 : 0;
     g.bias_stride = N;
     int64_t grid;
-    if (!set_grid(p, groups, group_rows(t), group_cols(t), grid)) return MMAC_ERR_UNSUPPORTED;
+    if (!set_grid(p, groups, t, GROUP_256, grid)) return MMAC_ERR_UNSUPPORTED;
     return launched(launch_gemm_grouped(a_type, trans_b != 0, t, p, g, grid, static_cast<hipStream_t>(stream)));
 }
 
@@ -220,7 +229,7 @@ mmac_status_t mmac_gemm_grouped_mx(mmac_dtype_t a_type, mmac_dtype_t b_type, int
     const int forced = forced_tile();
     GroupTile t = forced >= 0 ? (GroupTile)forced : mx_tile(groups, M, N, K);
     if (t == GROUP_32) t = GROUP_16;
-    if (t == GROUP_256) t = GROUP_128x256;   // the 256 x 256 tile has no registers left for the scale words
+    if (t == GROUP_256) t = kMxLargest;   // the 256 x 256 tile has no registers left for the scale words
     GemmParams p = make_params(M, N, K, alpha, A, lda, B, ldb / per, beta, C, ldc, D, ldd, ep);
     p.sa = SA;
     p.ldsa = ldsa;
@@ -235,7 +244,7 @@ mmac_status_t mmac_gemm_grouped_mx(mmac_dtype_t a_type, mmac_dtype_t b_type, int
     g.sb_stride = groups > 1 ? stride_sb : 0;
     g.bias_stride = N;
     int64_t grid;
-    if (!set_grid(p, groups, group_rows(t), t == GROUP_16 ? kMxRowsCols : group_cols(t), grid)) return MMAC_ERR_UNSUPPORTED;
+    if (!set_grid(p, groups, t, kMxLargest, grid)) return MMAC_ERR_UNSUPPORTED;
     return launched(launch_gemm_grouped_mx(a_type, b_type, t, p, g, grid, static_cast<hipStream_t>(stream)));
 }
 

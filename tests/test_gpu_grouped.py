@@ -203,6 +203,22 @@ def test_bad_offsets_stay_inside(bad):
     assert ((D == 5) | (D == K)).all()
 
 
+@pytest.mark.parametrize("G,N,K", [(80_000, 2048, 16), (34_000, 16384, 8)])
+def test_forward_of_many_tiles(G, N, K):
+    """A row a group and more workgroups than 2^21 (the second: than small tiles can be launched): every row meets its group's weights."""
+    gen = torch.Generator(device=dev()).manual_seed(G)
+    A = torch.randint(-2, 3, (G, K), device=dev(), generator=gen, dtype=torch.int8).to(torch.bfloat16)
+    B = torch.randint(-2, 3, (G, N, K), device=dev(), generator=gen, dtype=torch.int8).to(torch.bfloat16)    # 5.2 and 8.9 GB
+    o = torch.arange(G + 1, dtype=torch.int32, device=dev())
+    D = torch.full((G, N), 99.0, dtype=torch.bfloat16, device=dev())
+    mm.gemm_grouped(A, o, B, D)
+    for i in range(0, G, 5_000):
+        want = torch.zeros(min(5_000, G - i), N, device=dev())
+        for k in range(K):
+            want += A[i:i + 5_000, k:k + 1].float() * B[i:i + 5_000, :, k].float()
+        assert torch.equal(D[i:i + 5_000].float(), want), i                     # sums of at most 64: exact in bf16
+
+
 # ---- weight gradient ----------------------------------------------------------------------------
 
 def run_wgrad(rows, N, K, t, out=torch.float32, integers=False, alpha=1.0, beta=0.0, same=False, key=0):

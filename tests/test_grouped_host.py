@@ -113,6 +113,21 @@ def test_wgrad_of_many_tiles_is_not_refused(L, kw):
     assert wgrad(L, ldy=-(-N // 8) * 8, ldx=-(-K // 8) * 8, ldd=K, sd=N * K, **kw) == mm.ERR_HIP
 
 
+@no_gpu
+@pytest.mark.parametrize("kw", [
+    dict(G=16384, M=1 << 20, N=8192, K=64), dict(G=80_000, M=80_000, N=2048, K=16), dict(G=270_000, M=270_000, N=2048, K=8),
+    dict(G=16384, M=1 << 20, N=8192, K=64, trans=1), dict(G=4096, M=16384, N=16384, K=4096, tb=mm.FP4_E2M1),
+    dict(G=300_000, M=300_000, N=2048, K=32, tb=mm.FP8_E4M3), dict(G=1000, M=2 << 20, N=16384, K=64), dict(G=1, M=1 << 21, N=32768, K=64),
+])
+def test_forward_of_many_tiles_is_not_refused(L, kw):
+    kw = dict(kw)
+    N, K = kw["N"], kw["K"]
+    if "tb" in kw:
+        assert grouped_mx(L, lda=K, ldb=K, sb=N * K, ldsa=kw["M"], ldsb=N, ssb=-(-K // 128) * N, ldd=N, **kw) == mm.ERR_HIP
+    else:
+        assert grouped(L, lda=K, ldb=N if kw.get("trans") else K, sb=N * K, ldd=N, **kw) == mm.ERR_HIP
+
+
 def test_empty_is_a_no_op(L):
     for kw in (dict(G=0), dict(M=0), dict(N=0)):
         assert grouped(L, A=None, B=None, D=None, off=None, **kw) == OK
