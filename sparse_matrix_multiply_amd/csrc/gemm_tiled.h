@@ -226,13 +226,19 @@ struct TiledGemm {
         col0 = tn * BN;
         set_operands();
         if constexpr (SCALED) {
-            rsa = make_rsrc(p.sa + row_base + row0, (uint32_t)((p.scale_rows * p.ldsa - row_base - row0) * 4));
-            rsb = make_rsrc(p.sb + col0, (uint32_t)((p.scale_rows * p.ldsb - col0) * 4));
+            rsa = scale_words(p.sa + row_base + row0, p.ldsa, p.M - row0);
+            rsb = scale_words(p.sb + col0, p.ldsb, p.N - col0);
         }
 #pragma unroll
         for (int i = 0; i < TM; ++i)
 #pragma unroll
             for (int j = 0; j < TN; ++j) acc[i][j] = acc_t{};
+    }
+
+    // The scale words of a tile's rows or columns, `left` of them to the matrix's end: nothing past the last one's last word is
+    // read, where the array may end (a view that begins inside its rows).
+    __device__ __forceinline__ rsrc_t scale_words(const uint32_t *at, int64_t ld, int left) const {
+        return make_rsrc(at, p.scale_rows > 0 ? (uint32_t)(((p.scale_rows - 1) * ld + left) * 4) : 0u);
     }
 
     // Buffers over this tile's part of A, B and the index words.

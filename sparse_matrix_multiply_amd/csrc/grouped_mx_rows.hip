@@ -46,8 +46,9 @@ __global__ __launch_bounds__(512) void gemm_grouped_mx_rows_kernel(GemmParams p,
     const int words = p.scale_rows, b_end = FB == 4 ? p.K / 2 : p.K;   // bytes of a row
     const rsrc_t ra = make_rsrc(p.A, (uint32_t)(p.M * p.a_pitch));
     const rsrc_t rb = make_rsrc(p.B + (int64_t)col0 * p.b_pitch, (uint32_t)(cols * p.b_pitch));
-    const rsrc_t rsa = make_rsrc(p.sa + at.first + at.top, (uint32_t)((words * p.ldsa - at.first - at.top) * 4));
-    const rsrc_t rsb = make_rsrc(p.sb + at.g * q.sb_stride + col0, (uint32_t)((words * p.ldsb - col0) * 4));
+    // scale words to the last strip's last one of these rows and columns: the arrays may end there
+    const auto strips_of = [&](const uint32_t *w, int64_t ld, int n) { return make_rsrc(w, words > 0 ? (uint32_t)(((words - 1) * ld + n) * 4) : 0u); };
+    const rsrc_t rsa = strips_of(p.sa + at.first + at.top, p.ldsa, p.M), rsb = strips_of(p.sb + at.g * q.sb_stride + col0, p.ldsb, cols);
     SkinnyOut<float, 1, 2, R::kWaves> out(p, col0);
 
     f32x4 acc[1][2] = {};

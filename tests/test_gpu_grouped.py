@@ -510,6 +510,29 @@ def test_mx_exponents_far_apart(tile, kb, out, monkeypatch):
     check_sums(got, want, mags, K, OUT[out], 2.0 ** -13)
 
 
+@pytest.mark.parametrize("tile", [16, 64, 128, 1282])
+@pytest.mark.parametrize("out", ["fp32", "bf16"])
+def test_mx_scale_words_at_the_end_of_their_arrays(tile, out, monkeypatch):
+    """Scale words as columns of a wider array, whose last row ends with the last word that is used."""
+    monkeypatch.setenv("MMAC_TILE", str(tile))
+    g = rng("words", tile, out)
+    sizes, N, K = [50, 3, 0, 87], 101, 416
+    o, M = offsets(sizes, 0, 0)
+    G = len(sizes)
+    ca, ea, a = mx8_operand(g, (M, K), "e4m3", True)
+    cb, eb, b = mx8_operand(g, (G * N, K), "fp4", True)
+    A = torch.from_numpy(ca).to(dev()).view(torch.float8_e4m3fn)
+    B = torch.from_numpy((cb[:, 0::2] | (cb[:, 1::2] << 4)).reshape(G, N, K // 2)).to(dev())
+    words = np.stack([R.sx_words(eb[i * N:(i + 1) * N], 255) for i in range(G)])
+    SA = torch.nn.functional.pad(torch.from_numpy(R.sx_words(ea, 255)).to(dev()), (37, 0), value=-1)[:, 37:]
+    SB = torch.nn.functional.pad(torch.from_numpy(words).to(dev()), (29, 0), value=-1)[:, :, 29:]
+    D = torch.empty(M, N, dtype=OUT[out], device=dev())
+    mm.gemm_grouped_mx(A, SA, torch.from_numpy(o).to(dev()), B, SB, D, b_type=mm.FP4_E2M1)
+    for i in range(G):
+        r = slice(o[i], o[i + 1])
+        assert np.array_equal(f64(D[r]), torch.from_numpy(a[r] @ b[i * N:(i + 1) * N].T).to(OUT[out]).double().numpy()), f"group {i}"
+
+
 def test_mx_of_zero_length():
     D = torch.full((4, 8), 5.0, device=dev())
     e = torch.empty(4, 0, dtype=torch.float8_e4m3fn, device=dev())
