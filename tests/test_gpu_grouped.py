@@ -187,6 +187,35 @@ def test_other_groups_do_not_leak():
         assert torch.isnan(W[1]).all() and torch.isfinite(W[0]).all() and torch.isfinite(W[2]).all()
 
 
+@pytest.mark.parametrize("tile", [None, 16, 32, 64, 128, 1282, 256])
+@pytest.mark.parametrize("trans", [False, True])
+def test_other_groups_do_not_leak_in_any_tile(tile, trans, monkeypatch):
+    """NaN in one group's rows, weights or bias stays there: whole and half tiles of 150 and 300 rows beside the group's own, K in the
+    middle of a k-tile."""
+    if tile is not None:
+        monkeypatch.setenv("MMAC_TILE", str(tile))
+    g = rng("leak", trans)
+    K, N, o = 200, 280, np.cumsum([0, 150, 20, 300, 45, 130]).astype(np.int32)
+    a, b = g.standard_normal((o[-1], K)), g.standard_normal((5, N, K))
+    rows = np.zeros(o[-1], bool)
+    for i in (1, 3):
+        rows[o[i]:o[i + 1]] = True
+        b[i] = np.nan
+    a[rows] = np.nan
+    bias = torch.zeros(5, N, device=dev())
+    bias[1] = float("nan")
+    A, off = pitched(a, torch.bfloat16), torch.from_numpy(o).to(dev())
+    B = matrices(np.swapaxes(b, 1, 2) if trans else b, torch.bfloat16)
+    for t in (torch.float32, torch.bfloat16):
+        D = torch.empty(int(o[-1]), N, dtype=t, device=dev())
+        mm.gemm_grouped(A, off, B, D, trans_b=trans, bias=bias)
+        bad = torch.isnan(D).cpu().numpy()
+        assert bad[rows].all() and not bad[~rows].any()
+        W = torch.empty(5, N, K, dtype=t, device=dev())
+        mm.gemm_grouped_wgrad(pitched(g.standard_normal((o[-1], N)), torch.bfloat16), A, off, W)
+        assert torch.isnan(W[[1, 3]]).all() and torch.isfinite(W[[0, 2, 4]]).all()
+
+
 @pytest.mark.parametrize("bad", [[0, 40, 20, 64], [-5, 10, 30, 64], [0, 10, 1000, 2000], [70, 80, 90, 100], [2 ** 31 - 1, -(2 ** 31), 5, 2 ** 31 - 1]])
 def test_bad_offsets_stay_inside(bad):
     """Offsets that decrease or leave the arrays: nothing outside them is touched."""
