@@ -329,7 +329,7 @@ mmac_status_t mmac_gemm_dense_static(mmac_dtype_t a_type, mmac_dtype_t b_type,
  *                   ldsa % 4 == 0, SA 16-byte aligned.  Bytes of blocks at or
  *                   past K/32 are ignored.
  *   SB              the same for the N columns of B (ldsb >= N).
- *   e = 255 (NaN in E8M0) in a block that is used gives unspecified results.
+ *   e = 255 (NaN in E8M0) in a block that is used gives NaN in the outputs whose sums hold it.
  *   C, D, ep, stream and the error rules as in mmac_gemm_dense_ep.  Outputs
  *   with M <= 32 rows use the tiled kernel (there is no skinny path here).
  */

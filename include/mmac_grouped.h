@@ -53,7 +53,7 @@ mmac_status_t mmac_gemm_grouped(mmac_dtype_t a_type, int trans_b, int64_t groups
  *             are at SB + g * stride_sb, ceil(K/128) x ldsb, ldsb >= N, 4-byte aligned.
  *             Each array (a group's, for B) spans less than 2^31 bytes.
  *   lda, ldb, stride_b count elements (FP4: two per byte; rows start on 16 bytes).
- * e = 255 in a block that is used gives unspecified results.
+ * e = 255 (NaN) in a block that is used gives NaN in the outputs whose sums hold it.
  * Sums are fp32.  Outputs of 16 and 8 bits come from the block-scaled matrix instructions,
  * for any exponents; they add up the 64 or 128 products of an instruction with fewer bits than
  * fp32, an error of up to 2^-13 of the sum of the magnitudes before the output is rounded.  Where the

@@ -20,7 +20,7 @@ extern "C" {
  * multiple of 16; SX as in mmac_lowbit.h).  Exponents as in mmac_mx8_quantize with T = 6;
  * each element is the E2M1 value nearest to x * 2^(127-e), ties to the even code, with
  * x's sign.  Nothing saturates.  A block that holds a NaN or an infinity gets e = 255
- * and zero codes.  Codes past K are zero.
+ * and zero codes, which is NaN to both products.  Codes past K are zero.
  */
 mmac_status_t mmac_mx4_quantize(mmac_dtype_t x_type, int64_t M, int64_t K, const void *X, int64_t ldx, void *Xq,
                                 int64_t pitch, uint32_t *SX, int64_t lds, void *stream);
