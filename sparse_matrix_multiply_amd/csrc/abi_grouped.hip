@@ -56,11 +56,14 @@ GroupTile input_tile(int64_t groups, int64_t M, int64_t N, int64_t K) {
     return GROUP_128;
 }
 // Block-scaled: a 128 x 128 tile's stages are small enough for two or three workgroups a compute unit (FP4 weights, 4 x 2048 x 4096^2:
-// 142 against 164 in 128 x 256; 16 x 64: 51 against 47; 16 x 16: 39 against 31).
+// 142 against 164 in 128 x 256; 16 x 64: 51 against 47; 16 x 16: 39 against 31).  16 rows x 32 columns also for up to 32 rows and few
+// tiles (kernel time, 8 x 32 x 1024 x 2048 E4M3, 128 tiles of 64 x 64: 7.9 against 11.5; 4 x 32 x 4096 x 2048 FP4, 256 of them: 11.6
+// against 11.3).  64 x 64 for short sums of groups that a tile of 128 rows would leave half empty (FP4, N 4096, K 1024: 16 x 64 12.6,
+// 16 in 128 x 256; 16 x 128 20.6 against 17.3; 4 x 2048 67 against 51 in 128 x 128) or too few of those.
 GroupTile mx_tile(int64_t groups, int64_t M, int64_t N, int64_t K) {
     const int64_t rows = (M + groups - 1) / groups, small = even_tiles(groups, M, N, GROUP_64);
     if ((rows <= 8 && (K > 2048 || small <= 256)) || (rows <= 32 && small <= 128)) return GROUP_16;
-    if (K <= 1152 || even_tiles(groups, M, N, GROUP_128) < 256) return GROUP_64;
+    if ((rows <= 64 && K <= 1152) || even_tiles(groups, M, N, GROUP_128) < 256) return GROUP_64;
     return rows <= 128 && even_tiles(groups, M, N, GROUP_128x256) >= 192 ? GROUP_128x256 : GROUP_128;
 }
 
