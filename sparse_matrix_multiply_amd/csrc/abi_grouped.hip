@@ -48,7 +48,7 @@ GroupTile forward_tile(int64_t groups, int64_t M, int64_t N, int64_t K) {
 }
 // Weights read as K x N rows (K: the sum).  128 x 128, two workgroups a compute unit, up to 512 rows (16 x 128 x 4096^2: 184 against 208 in
 // 256 x 256; 8 x 512 x 8192 x 2048: 299 against 258), 64 x 64 for short sums or too few tiles (11 x 163, 1452 columns, K 6313: 113
-// against 142).
+// against 142; K 2048, 2048 columns: 16 x 128, 256 tiles, 38 against 40; 24 x 128, 384 of them, 54 against 41).
 GroupTile input_tile(int64_t groups, int64_t M, int64_t N, int64_t K) {
     const int64_t rows = (M + groups - 1) / groups;
     if (rows >= 512 && even_tiles(groups, M, N, GROUP_256) >= 192) return GROUP_256;
@@ -68,10 +68,11 @@ GroupTile mx_tile(int64_t groups, int64_t M, int64_t N, int64_t K) {
 }
 
 // Weight gradients (us; a group's D is N x K, its sum M / groups rows long).  64 x 64, four or five workgroups a compute unit, hide
-// short sums' latencies and lose least at the edges (49 x 1109 x 1775 bf16 from 20 rows each: 178, in 256 x 256 237; 7 x 1965 x 1924
-// fp32 from 4: 42 against 63).  256 x 256 for long sums (4 x 4096^2 from 2048 rows: 290 against 441) and, where they fill their tiles, for
-// many large matrices in 16 bits (16 x 4096^2 from 32 rows: 204 against 241); those in fp32, whose C and D take the time, in 128 x 128 (440,
-// 473 in 256 x 256).
+// short sums' latencies and lose least at the edges (49 x 1109 x 1775 bf16 from 20 rows each, tiles 0.86 full: 178, in 256 x 256 237;
+// 7 x 1965 x 1924 fp32 from 4: 42 against 63).  256 x 256 for long sums that fill their tiles (4 x 4096^2 from 2048 rows: 290 against
+// 441; 4 x 1850^2 from 1024, 0.82 full: 46 against 55; 8 x 1300^2 from 512, 0.72 full: 54 against 42) and, where they fill them better
+// still, for many large matrices in 16 bits (16 x 4096^2 from 32 rows: 204 against 241; 24 x 2700^2 from 64, 0.92 full: 154 against 171);
+// those in fp32, whose C and D take the time, in 128 x 128 (440, 473 in 256 x 256).
 GroupTile wgrad_tile(int64_t groups, int64_t M, int64_t N, int64_t K, int64_t tiles, bool fp32) {
     const int64_t rows = M / groups;
     const double filled = (double)groups * N * K / (65536.0 * tiles);   // share of the 256 x 256 tiles that is D

@@ -66,7 +66,7 @@ enum : int { HALF_NONE, HALF_IN_PLACE, HALF_LAST };
 
 // Workgroup -> (group, tile), from the offsets alone.  Every wave looks for itself, 64 * PER groups at a time: a lane has PER
 // neighbouring ones (their offsets are loaded together), their tile rows, and the sum of those before it.  Four a lane for more
-// than 64 groups (8 rows through 256 experts of 2048^2: 23 us, 28 with 64 groups at a time), one up to 64 (16 rows through 64 experts
+// than 64 groups (8 rows through 256 experts of 2048^2: 22 us, 28 with 64 groups at a time), one up to 64 (16 rows through 64 experts
 // in 4 bits: 32.2 us, 33.9 with four).  Tiles are BM rows high; whole ones and those of HALF_LAST
 // are numbered each group by group, within a group in bands of group_m tile rows, column by column, and dealt to the
 // XCDs in contiguous runs, so tiles that share a group's weights run at about the same time on one L2.  Returns false
@@ -77,7 +77,7 @@ __device__ __forceinline__ bool find_group_tile_by(const Groups &q, int tiles_n,
     const int lane = threadIdx.x & 63;
     const auto whole = [](int rows) { return (rows + (HALF == HALF_LAST ? BM / 2 : BM) - 1) / BM; };
     const auto half = [](int rows) { return rows % BM > 0 && rows % BM <= BM / 2 ? 1 : 0; };
-    // the lane's groups of the 256 from `base` on; those behind the last one have no rows
+    // the lane's groups of the 64 * PER from `base` on; those behind the last one have no rows
     const auto load = [&](int base, int (&first)[PER], int (&rows)[PER]) {
         int o[PER + 1];
 #pragma unroll
