@@ -100,7 +100,9 @@ void gemm_grouped_wgrad_kernel(GemmParams p, Groups q) {
 template <class Op>
 hipError_t launch_grouped_op(GroupTile tile, const GemmParams &p, const Groups &g, int64_t blocks, hipStream_t s) {
     const dim3 grid((unsigned)blocks);
-    // workgroups of the small tiles that fit a compute unit's 160 KiB of LDS
+    // workgroups of the small tiles that fit a compute unit's 160 KiB of LDS.  Three of 128 x 128 (FP4 weights) leave 168 registers a
+    // wave, 25 too few (22 in the fp32 form), which are spilled and reloaded in the loop of the last k-tiles, not in the steady one; two,
+    // without spills, are as fast within noise (us, three / two: 4 x 2048 x 4096^2 128 / 135; 16 x 256 x 4096 x 8192 171 / 167, fp32 231 / 236)
     constexpr int L64 = TiledGemm<Op, 64, 64, 2, 2, 2>::LDS_BYTES, L128 = TiledGemm<Op, 128, 128, 2, 2, 2>::LDS_BYTES;
     constexpr int P64 = 160 * 1024 / L64 < 4 ? 160 * 1024 / L64 : 4, P128 = 160 * 1024 / L128 < 3 ? 160 * 1024 / L128 : 3;
     switch (tile) {

@@ -5,7 +5,8 @@
 // written once.  Rows longer than 32768 are walked twice, the second time from the caches.
 // Sums, rstd and the products of y are fp32; y itself is rounded once, to its output type.
 //
-// HBM bounds it: 8192^2 bf16 with a residual to E4M3 moves 472 MB in 91 us (5.2 TB/s; a large copy reaches 5.0).  256 threads with four
+// HBM bounds it, but for rows of up to 256, which leave lanes of their wave without elements (2^20 x 128 331 us, 3.2 TB/s; 2^18 x 256
+// 111, 4.8): 8192^2 bf16 with a residual to E4M3 moves 472 MB in 91 us (5.2 TB/s; a large copy reaches 5.0).  256 threads with four
 // groups and the weight read again for every row took 112 us, before the weight stayed in registers and 16-bit values were
 // converted in pairs.  One row of 4096 takes 2.8 us, all of it latency: the weight is loaded with the row (5.4 us when
 // it was loaded after the sum).  Consecutive rows run on one XCD, so their scale words, 4 bytes a row in each line, meet
