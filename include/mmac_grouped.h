@@ -3,7 +3,7 @@
  * has a weight matrix of its own, and where the groups begin is known in GPU
  * memory only.  Part of libmmac.so; the conventions of mmac.h (layouts, alignment,
  * memory, asynchrony, errors, thread safety, alpha and beta) hold here too; an
- * operand without elements may be NULL.
+ * operand without elements may be NULL and of any pitch.
  *
  *   groups   their number G, at most 2^30 (MMAC_ERR_UNSUPPORTED beyond).
  *   offsets  G + 1 32-bit integers in device memory, not decreasing, from 0 to M:

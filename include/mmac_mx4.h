@@ -2,7 +2,7 @@
  * mmac, 4-bit block-scaled operands: packed FP4_E2M1 elements with one E8M0 scale
  * per 32 consecutive elements of a row.  Part of libmmac.so; the conventions of mmac.h
  * (layouts, alignment, memory, asynchrony, errors, thread safety) hold here too; an
- * operand without elements may be NULL.
+ * operand without elements may be NULL and of any pitch.
  */
 #ifndef MMAC_MX4_H
 #define MMAC_MX4_H

@@ -5,7 +5,7 @@
  * mmac_gemm_dense_mx, mmac_gemm_grouped_mx and mmac_gemm_mx8_wgrad read; and its
  * gradients.  Part of libmmac.so; the conventions of mmac.h (alignment, memory,
  * asynchrony, errors, thread safety) hold here too; an operand without elements
- * may be NULL.  Every matrix is row-major M x N with 16-byte alignment and pitch,
+ * may be NULL and of any pitch.  Every matrix is row-major M x N with 16-byte alignment and pitch,
  * ld in elements; N is the length that is normed, M the number of rows.
  */
 #ifndef MMAC_NORM_H

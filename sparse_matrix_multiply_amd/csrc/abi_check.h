@@ -32,6 +32,11 @@ inline mmac_status_t check_rows(const void *p, int64_t ld, int64_t cols, int es)
     return MMAC_OK;
 }
 
+// The same of a matrix of `rows` rows: one without elements is not read, and its pitch says nothing.
+inline mmac_status_t check_matrix(const void *p, int64_t ld, int64_t rows, int64_t cols, int es) {
+    return rows == 0 || cols == 0 ? MMAC_OK : check_rows(p, ld, cols, es);
+}
+
 // A scale array of `rows` rows of ld words, `cols` of them used.
 inline mmac_status_t check_words(const void *p, int64_t ld, int64_t rows, int64_t cols) {
     if (ld < cols || ld < 1) return MMAC_ERR_INVALID_ARG;

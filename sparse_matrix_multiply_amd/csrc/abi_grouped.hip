@@ -177,8 +177,8 @@ mmac_status_t mmac_gemm_grouped(mmac_dtype_t a_type, int trans_b, int64_t groups
     if (!empty && K > 0 && (!A || !B)) return MMAC_ERR_INVALID_ARG;
     const int64_t b_rows = trans_b ? K : N, b_cols = trans_b ? N : K;
     if (K > 0) {   // else neither is read
-        st = check_rows(A, lda, K, 2);
-        if (st == MMAC_OK) st = check_rows(B, ldb, b_cols, 2);
+        st = check_matrix(A, lda, M, K, 2);
+        if (st == MMAC_OK) st = check_matrix(B, ldb, groups * b_rows, b_cols, 2);
         if (st == MMAC_OK) st = check_stride(groups, b_rows, b_cols, ldb, stride_b, 8);
     }
     if (st == MMAC_OK) st = check_out(groups > 0 ? M : 0, N, alpha, beta, C, ldc, D, ldd, ep);
@@ -219,8 +219,8 @@ mmac_status_t mmac_gemm_grouped_mx(mmac_dtype_t a_type, mmac_dtype_t b_type, int
     if (K > 0) {   // else none of the four is read
         if (ldb < K || ldb < 1) return MMAC_ERR_INVALID_ARG;
         if (ldb % per || stride_b % per) return MMAC_ERR_MISALIGNED;
-        st = check_rows(A, lda, K, 1);
-        if (st == MMAC_OK) st = check_rows(B, ldb / per, K / per, 1);
+        st = check_matrix(A, lda, M, K, 1);
+        if (st == MMAC_OK) st = check_matrix(B, ldb / per, groups * N, K / per, 1);
         if (st == MMAC_OK) st = check_stride(groups, N, K, ldb, stride_b, 16 * per);
         if (st == MMAC_OK) st = check_words(SA, ldsa, strips, M);
         if (st == MMAC_OK) st = check_words(SB, ldsb, strips, N);
@@ -266,8 +266,8 @@ mmac_status_t mmac_gemm_grouped_wgrad(mmac_dtype_t y_type, int64_t groups, int64
     mmac_status_t st = check_out(groups > 0 ? N : 0, K, alpha, beta, C, ldc, D, ldd, ep);
     if (st != MMAC_OK) return st;
     if (ep.act != MMAC_ACT_NONE || ep.bias) return MMAC_ERR_UNSUPPORTED;
-    st = check_rows(dY, ldy, N, 2);
-    if (st == MMAC_OK) st = check_rows(X, ldx, K, 2);
+    st = check_matrix(dY, ldy, M, N, 2);
+    if (st == MMAC_OK) st = check_matrix(X, ldx, M, K, 2);
     if (st == MMAC_OK) st = check_stride(groups, N, K, ldd, stride_d, 1);
     if (st == MMAC_OK && beta != 0.0) st = check_stride(groups, N, K, ldc, stride_c, 1);
     if (st != MMAC_OK) return st;
@@ -282,6 +282,7 @@ mmac_status_t mmac_gemm_grouped_wgrad(mmac_dtype_t y_type, int64_t groups, int64
     // so many tiles that only larger ones can be launched
     while (t != GROUP_256 && !grid_fits(wgrad_blocks(per(t), groups), t)) t = t == GROUP_64 ? GROUP_128 : GROUP_256;
     if (!grid_fits(wgrad_blocks(per(t), groups), t)) return MMAC_ERR_UNSUPPORTED;
+    if (M == 0) ldy = ldx = 8;   // nothing is read
     GemmParams p = make_params(N, K, 0, alpha, dY, ldy * 2, X, ldx * 2, beta, C, ldc, D, ldd, ep);
     p.tiles_m = (int)((N + group_rows(t) - 1) / group_rows(t));
     p.tiles_n = (int)((K + group_cols(t) - 1) / group_cols(t));

@@ -213,8 +213,8 @@ mmac_status_t mmac_mx4_quantize(mmac_dtype_t x_type, int64_t M, int64_t K, const
     if (!is_input(x_type)) return MMAC_ERR_UNSUPPORTED;
     if (bad_dim(M) || bad_dim(K)) return MMAC_ERR_INVALID_ARG;
     if (M > 0 && K > 0 && (!X || !Xq || !SX)) return MMAC_ERR_INVALID_ARG;
-    mmac_status_t st = check_rows(X, ldx, K, elem_size(x_type));
-    if (st == MMAC_OK) st = check_rows(Xq, pitch, (K + 31) / 32 * 16, 1);
+    mmac_status_t st = check_matrix(X, ldx, M, K, elem_size(x_type));
+    if (st == MMAC_OK) st = check_matrix(Xq, pitch, M, (K + 31) / 32 * 16, 1);
     if (st == MMAC_OK) st = check_words(SX, lds, (K + 127) / 128, M);
     if (st != MMAC_OK || M == 0 || K == 0) return st;
     return launched(launch_mx4_quantize(x_type, mx8_params(x_type, M, K, X, ldx, Xq, pitch, SX, lds),

@@ -31,10 +31,10 @@ mmac_status_t mmac_rmsnorm(mmac_dtype_t x_type, mmac_dtype_t w_type, mmac_dtype_
     if (y_type != x_type && !low) return MMAC_ERR_UNSUPPORTED;
     if (!std::isfinite(eps) || eps < 0.0 || eps > (double)FLT_MAX) return MMAC_ERR_INVALID_ARG;
     if (M > 0 && N > 0 && (!X || !w || !Y || (low && !SY))) return MMAC_ERR_INVALID_ARG;
-    st = check_rows(X, ldx, N, es);
-    if (st == MMAC_OK && residual) st = check_rows(residual, ldr, N, es);
-    if (st == MMAC_OK && H) st = check_rows(H, ldh, N, es);
-    if (st == MMAC_OK) st = check_rows(Y, ldy, low ? (N + 31) / 32 * 32 : N, low ? 1 : es);
+    st = check_matrix(X, ldx, M, N, es);
+    if (st == MMAC_OK && residual) st = check_matrix(residual, ldr, M, N, es);
+    if (st == MMAC_OK && H) st = check_matrix(H, ldh, M, N, es);
+    if (st == MMAC_OK) st = check_matrix(Y, ldy, M, low ? (N + 31) / 32 * 32 : N, low ? 1 : es);
     if (st == MMAC_OK && low) st = check_words(SY, lds, (N + 127) / 128, M);
     if (st != MMAC_OK) return st;
     // outputs in an input's place
@@ -69,10 +69,10 @@ mmac_status_t mmac_rmsnorm_grad(mmac_dtype_t x_type, mmac_dtype_t w_type, int64_
     mmac_status_t st = check_types(x_type, w_type, M, N);
     if (st != MMAC_OK) return st;
     if (workspace_bytes < 0 || (M > 0 && N > 0 && (!dY || !H || !w || !rstd || !dX))) return MMAC_ERR_INVALID_ARG;
-    st = check_rows(dY, lddy, N, es);
-    if (st == MMAC_OK) st = check_rows(H, ldh, N, es);
-    if (st == MMAC_OK && dH) st = check_rows(dH, lddh, N, es);
-    if (st == MMAC_OK) st = check_rows(dX, lddx, N, es);
+    st = check_matrix(dY, lddy, M, N, es);
+    if (st == MMAC_OK) st = check_matrix(H, ldh, M, N, es);
+    if (st == MMAC_OK && dH) st = check_matrix(dH, lddh, M, N, es);
+    if (st == MMAC_OK) st = check_matrix(dX, lddx, M, N, es);
     if (st != MMAC_OK) return st;
     if (dX && ((dX == dY && lddx != lddy) || (dX == dH && lddx != lddh) || dX == H)) return MMAC_ERR_INVALID_ARG;
     if (!aligned(w, 16) || !aligned(rstd, 4) || !aligned(dW, 16) || !aligned(workspace, 16)) return MMAC_ERR_MISALIGNED;

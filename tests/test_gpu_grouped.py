@@ -562,6 +562,25 @@ def test_mx_scale_words_at_the_end_of_their_arrays(tile, out, monkeypatch):
         assert np.array_equal(f64(D[r]), torch.from_numpy(a[r] @ b[i * N:(i + 1) * N].T).to(OUT[out]).double().numpy()), f"group {i}"
 
 
+def test_matrices_without_elements():
+    """New tensors without rows or columns, whose pitches are no multiple of 16 bytes."""
+    def e(*shape):
+        return torch.empty(*shape, dtype=torch.bfloat16, device=dev())
+
+    o = torch.tensor([0, 1, 3], dtype=torch.int32, device=dev())
+    none = torch.zeros(3, dtype=torch.int32, device=dev())
+    mm.gemm_grouped(e(3, 16), o, e(2, 16, 0), e(3, 0), trans_b=True)
+    mm.gemm_grouped(e(0, 33), none, e(2, 8, 40)[:, :, :33], e(0, 8))
+    D = torch.full((3, 8), 5.0, device=dev())
+    mm.gemm_grouped(e(3, 0), o, e(2, 8, 0), D)
+    assert (D == 0).all()
+    mm.gemm_grouped_wgrad(e(3, 0), e(3, 16), o, torch.empty(2, 0, 16, device=dev()))
+    mm.gemm_grouped_wgrad(e(3, 16), e(3, 0), o, torch.empty(2, 16, 0, device=dev()))
+    D, C = torch.full((2, 33, 5), 5.0, device=dev()), torch.ones(2, 33, 5, device=dev())
+    mm.gemm_grouped_wgrad(e(0, 33), e(0, 5), none, D, beta=2.0, C=C)
+    assert (D == 2).all()
+
+
 def test_mx_of_zero_length():
     D = torch.full((4, 8), 5.0, device=dev())
     e = torch.empty(4, 0, dtype=torch.float8_e4m3fn, device=dev())

@@ -278,6 +278,21 @@ def test_gradient_without_rows_reads_no_workspace(N):
     assert (dW[:N] == 0).all() and (dW[N:] == 5).all()
 
 
+@pytest.mark.parametrize("t", list(TYPES))
+def test_without_elements(t):
+    """New tensors without rows or columns, whose pitches are no multiple of 16 bytes: nothing to do but a dW of zeros."""
+    t = TYPES[t]
+    for M, N in ((0, 33), (4, 0), (0, 0)):
+        x, w, r = (torch.empty(M, N, dtype=t, device=dev()) for _ in range(5)), torch.ones(N, device=dev()), torch.empty(M, device=dev())
+        x, y, h, q, d = x
+        mm.rmsnorm(x, w, y, residual=q, H=h, rstd=r)
+        dW = torch.full((N,), 5.0, device=dev())
+        mm.rmsnorm_grad(y, h, w, r, d, dW=dW, dH=q, workspace=mm.rmsnorm_grad_workspace(M, max(N, 1), dev()))
+        assert (dW == 0).all()
+        codes = torch.empty(M, -(-N // 32) * 16, dtype=torch.uint8, device=dev())
+        mm.mx4_quantize(x, codes, torch.empty(-(-N // 128), M, dtype=torch.int32, device=dev()))
+
+
 @pytest.mark.parametrize("N", [40, 1500, 9000, 16384, 16388, 40000])
 def test_gradient_without_rows_or_pointers(N):
     ws = torch.full_like(mm.rmsnorm_grad_workspace(0, N, dev()), 255)

@@ -98,6 +98,15 @@ def test_gemm_grouped_wgrad_argument_errors(L, kw, code):
     assert wgrad(L, **kw) == code
 
 
+def test_matrices_without_elements_have_any_pitch(L):
+    """As torch has them: rows of nothing lie one element apart, no rows any number of elements."""
+    assert grouped(L, M=0, K=100, lda=100, ldb=104) == OK
+    assert grouped(L, G=0, K=100, lda=104, ldb=100) == OK
+    assert grouped(L, N=0, trans=1, ldb=1, sb=1, ldd=1) == OK
+    assert grouped(L, N=0, ldd=1, sb=0) == OK
+    assert wgrad(L, N=0, ldy=1, sd=0) == OK and wgrad(L, K=0, ldx=1, ldd=1, sd=0) == OK
+
+
 # On a machine without a GPU the launch itself is what fails: the call was not refused.
 no_gpu = pytest.mark.skipif(torch.cuda.is_available(), reason="the pointers are fake: the calls would run")
 

@@ -114,6 +114,17 @@ def test_mx4_quantize_empty_is_a_no_op(L):
     assert quantize(L, K=0, X=None, Xq=None, SX=None) == OK
 
 
+def test_matrices_without_elements_have_any_pitch(L):
+    """As torch has them: rows of nothing lie one element apart, no rows any number of elements."""
+    assert norm(L, M=0, N=33, ldx=33, ldy=33) == OK
+    assert grad(L, M=0, N=33, lddy=33, ldh=33, lddx=33) == OK
+    assert quantize(L, M=0, K=33, ldx=33, pitch=33) == OK
+    assert norm(L, N=0, ldx=1, R=P, ldr=1, H=2 * P, ldh=1, Y=3 * P, ldy=1) == OK
+    assert norm(L, N=0, ldx=1, y=mm.BF8_E5M2, ldy=1, SY=P, lds=4) == OK
+    assert grad(L, N=0, lddy=1, ldh=1, dH=P, lddh=1, lddx=1, dW=P) == OK
+    assert quantize(L, K=0, ldx=1, pitch=1) == OK
+
+
 B16, F32, E4 = torch.bfloat16, torch.float32, torch.float8_e4m3fn
 
 
